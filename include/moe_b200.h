@@ -479,6 +479,94 @@ int moe_forward_kernel_count(void);
  * -1: null plan, or fp8 = 1 on a plan without FP8 regions. */
 int moe_plan_forward_launches(moe_plan_t plan, int fp8);
 
+/* ---- Operators around the layer: products grouped by expert, the dense layer,
+ * and the orthogonalised update of weight gradients. They need no plan. Each
+ * call runs on the calling thread's current device, enqueues on `stream` only
+ * and neither synchronises nor allocates, so it may be captured into a graph.
+ *
+ * Tensors are bf16 or fp16 (`dtype`; MOE_DTYPE_FP32 where stated), device
+ * memory, 16-byte aligned, the last index contiguous. A row pitch (ldx, ldy,
+ * ...) is given in elements: at least the row's length and a multiple of 8.
+ * K and N are multiples of 8 (rows of whole 16-byte chunks). Products are
+ * accumulated in fp32 on the tensor cores; a result is rounded once, to nearest.
+ *
+ * error_word: device int32 [1], or NULL. It is zeroed by the call and receives
+ * the call's device error code (0 = none, 1 = a bounded wait ran out,
+ * 2 = group offsets out of order or out of range).
+ *
+ * Common errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad pitch,
+ * unknown type or activation, negative count), MOE_ERR_UNSUPPORTED_SHAPE (K or N
+ * not a multiple of 8, too many groups), MOE_ERR_UNSUPPORTED_DEVICE, MOE_ERR_CUDA. */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2 } moe_dtype;
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,       /* z/2 (1 + erf(z / sqrt 2)) */
+  MOE_ACT_GELU_TANH = 3,  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} moe_activation;
+
+/* y[r] = x[r] W[e] for the rows offsets[e] <= r < offsets[e+1] of each group e
+ * (transpose = 0, W [groups, K, N]), or x[r] W[e]^T (transpose = 1,
+ * W [groups, N, K]: the input gradient of a product with the weights [K', N']
+ * taken as K = N', N = K'):
+ *   x [rows, K], y [rows, N]; offsets int32 [groups + 1] on the device, not
+ *   decreasing, inside 0 .. rows (moe_routing's expert_offset fits); groups may
+ *   be empty, sizes need no padding. Rows of y before offsets[0] and from
+ *   offsets[groups] on are left as they were. A group whose two offsets are out
+ *   of order or out of range is skipped and recorded in error_word.
+ * 1 <= groups <= 1024. ("MegaMoE 在 MoE 系统谱系中的位置", section 2.6: groups of
+ * any size without dropping; here also without padding.) */
+int moe_grouped_matmul(const void* x, long long ldx, const void* W, const int32_t* offsets, int rows, int groups, int K,
+                       int N, int transpose, int dtype, void* y, long long ldy, int32_t* error_word, void* stream);
+
+/* Weight gradient of moe_grouped_matmul: dW[e] = sum over the group's rows of
+ * x[r]^T dy[r], [groups, K, N] contiguous, overwritten; zeros for an empty (or
+ * skipped) group. x [rows, K], dy [rows, N]. */
+int moe_grouped_matmul_wgrad(const void* x, long long ldx, const void* dy, long long lddy, const int32_t* offsets,
+                             int rows, int groups, int K, int N, int dtype, void* dW, int32_t* error_word,
+                             void* stream);
+
+/* Dense layer: z = x W + bias, y = act(z) + residual.
+ *   x [T, K], W [K, N] contiguous, bias [N] or NULL, residual [T, N] or NULL,
+ *   y [T, N], preact [T, N] or NULL (receives z for moe_linear_backward). y may
+ *   be the residual itself (same pointer and pitch); no other overlap. T = 0
+ *   enqueues nothing but the error word's zeroing. */
+int moe_linear(const void* x, long long ldx, const void* W, const void* bias, const void* residual, long long ldr, int T,
+               int K, int N, int activation, int dtype, void* y, long long ldy, void* preact, long long ldz,
+               int32_t* error_word, void* stream);
+
+/* Gradients of moe_linear for the upstream dy [T, N]: dz = dy act'(preact),
+ * dx [T, K] = dz W^T, dW [K, N] = x^T dz, dbias [N] = sum_t dz (the residual's
+ * gradient is dy itself). dx, dW and dbias may each be NULL (not computed);
+ * W is needed for dx, x for dW, preact with an activation. dz is rounded to
+ * the tensors' type for the two products; dbias sums it unrounded.
+ * workspace: 256-byte aligned device memory of at least
+ * moe_linear_backward_workspace_bytes(T, N, activation, dbias != NULL) (may be
+ * NULL when that is 0). Further error: MOE_ERR_WORKSPACE_TOO_SMALL. */
+int moe_linear_backward(const void* dy, long long lddy, const void* x, long long ldx, const void* W, const void* preact,
+                        long long ldz, int T, int K, int N, int activation, int dtype, void* dx, long long lddx,
+                        void* dW, void* dbias, void* workspace, size_t workspace_bytes, int32_t* error_word,
+                        void* stream);
+size_t moe_linear_backward_workspace_bytes(int T, int N, int activation, int bias_grad);
+
+/* Orthogonalised update: for each matrix G [m, n] of the batch (any m, n;
+ * `dtype` bf16 or fp32, row pitch ldg >= n and batch pitch bsg in elements)
+ *   X = G / (|G|_F + eps);  `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X
+ * (X^T X on the right when m > n), with the step's a, b, c from the HOST array
+ * coeffs [steps, 3]; out bf16 [m, n] (pitches ldo, bso) receives the last X.
+ * X is carried as a pair of fp16 values (22 bits); A, bA + cAA and X enter the
+ * tensor-core products as fp16, accumulated in fp32; A and bA + cAA are stored
+ * times 1024, so their entries must stay below 64 in magnitude (with the usual
+ * quintic coefficients they stay below 7). A gradient of zeros gives zeros; an
+ * infinity or NaN in a matrix makes that matrix's output NaN and no other's.
+ * 1 <= steps <= 64; m, n <= 65536; batch <= 65535. workspace: 256-byte aligned,
+ * moe_orthogonalize_workspace_bytes(batch, m, n). */
+int moe_orthogonalize(const void* G, long long ldg, long long bsg, int batch, int m, int n, int dtype, int steps,
+                      const float* coeffs, float eps, void* out, long long ldo, long long bso, void* workspace,
+                      size_t workspace_bytes, int32_t* error_word, void* stream);
+size_t moe_orthogonalize_workspace_bytes(int batch, int m, int n);
+
 void moe_plan_destroy(moe_plan_t plan);
 const char* moe_status_string(int status);
 

@@ -26,6 +26,7 @@ STATUS_NAMES = {
 KERNEL_NAMES = ("router", "dispatch_scan", "dispatch_scatter", "expert_gemm", "finalize")
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
 
 
 class MoERouting(ctypes.Structure):
@@ -82,6 +83,19 @@ SIGNATURES = {
     "moe_plan_set_fp8": (_c_int, [_vp, _c_int]),
     "moe_forward_kernel_count": (_c_int, []),
     "moe_plan_forward_launches": (_c_int, [_vp, _c_int]),
+    "moe_grouped_matmul": (_c_int, [_vp, _c_ll, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_ll,
+                                    _vp, _vp]),
+    "moe_grouped_matmul_wgrad": (_c_int, [_vp, _c_ll, _vp, _c_ll, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
+                                          _vp, _vp]),
+    "moe_linear": (_c_int, [_vp, _c_ll, _vp, _vp, _vp, _c_ll, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_ll, _vp,
+                            _c_ll, _vp, _vp]),
+    "moe_linear_backward": (_c_int, [_vp, _c_ll, _vp, _c_ll, _vp, _vp, _c_ll, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                     _vp, _c_ll, _vp, _vp, _vp, _c_size, _vp, _vp]),
+    "moe_linear_backward_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "moe_orthogonalize": (_c_int, [_vp, _c_ll, _c_ll, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                   ctypes.POINTER(ctypes.c_float), ctypes.c_float, _vp, _c_ll, _c_ll, _vp, _c_size,
+                                   _vp, _vp]),
+    "moe_orthogonalize_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "moe_plan_destroy": (None, [_vp]),
     "moe_status_string": (ctypes.c_char_p, [_c_int]),
 }
@@ -466,3 +480,7 @@ def quantize_x_fp8(x: torch.Tensor, stream=None):
 
 def kernels_per_forward() -> int:
     return load_library().moe_forward_kernel_count()
+
+
+from .operators import (QUINTIC, grouped_matmul, grouped_matmul_wgrad, linear, linear_backward,  # noqa: E402
+                        orthogonalize)

@@ -9,7 +9,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
-SOURCES = [os.path.join(CSRC, "moe_b200.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("moe_b200.cu", "operators.cu")]
 DEPS = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
     os.path.join(os.path.dirname(HERE), "include", "moe_b200.h")]
 

@@ -1,0 +1,501 @@
+// C entry points of the operators around the MoE layer (include/moe_b200.h):
+// products grouped by expert, the dense layer and its backward, and the
+// orthogonalised update. Argument checks, tensor maps and launches; the
+// products run in tile_gemm.cuh, the element passes in operators.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/moe_b200.h"
+#include "common.cuh"
+#include "operators.cuh"
+#include "tile_gemm.cuh"
+
+using namespace moe;
+
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load();
+  if (f == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn.store(f = reinterpret_cast<EncodeFn>(p));
+  }
+  return f;
+}
+
+// A 16-bit operand: `inner` contiguous elements per row, `rows` rows of `pitch`
+// elements, `batch` such matrices `bs` elements apart.
+struct Operand {
+  const void* base;
+  uint64_t inner, rows, pitch, batch, bs;
+};
+
+bool map3(CUtensorMap* m, const Operand& o, uint32_t box_rows, bool f16) {
+  EncodeFn enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {o.inner, o.rows, o.batch};
+  const cuuint64_t strides[2] = {o.pitch * 2, (o.batch > 1 ? o.bs : o.pitch) * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.base),
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool set_maps(TgParams& p, const Operand& P, bool p_mn, const Operand& Q, bool q_mn) {
+  const bool h = p.f16 != 0;
+  bool ok = map3(&p.tm_p, P, p_mn ? 64 : 128, h);
+  if (q_mn) return ok && map3(&p.tm_q[0], Q, 64, h);
+  for (int i = 0; i < 4; ++i) ok = ok && map3(&p.tm_q[i], Q, 128u >> i, h);
+  return ok;
+}
+
+constexpr int kMaxDevices = 64;
+
+int current_device(int* num_sms) {
+  static std::atomic<int> sms[kMaxDevices];
+  int d = -1;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return -1;
+  int v = sms[d].load();
+  if (v == 0) {
+    int major = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, d) != cudaSuccess)
+      return -1;
+    sms[d].store(v = major == 10 ? v : -1);
+  }
+  *num_sms = v;
+  return d;
+}
+
+// Stages that fit for the largest N tile (`nt`) of a launch.
+void size_stages(TgParams& p, bool q_mn) {
+  const int half = p.nt / 2;
+  p.stage_bytes = kTgABytes + (q_mn ? (half + 63) / 64 * 8192 : half * 128);
+  p.stages = std::min(kTgMaxStages, kTgSmemTiles / p.stage_bytes);
+}
+
+// One launch. `tiles`: output tiles where the host knows them, else 0 (the
+// grid then covers every pair of SMs). Returns a moe_status.
+template <int Mode, bool PMn, bool QMn, int Epi, typename T>
+int launch(TgParams& p, long long tiles, bool pdl, cudaStream_t st) {
+  static std::atomic<int> clusters[kMaxDevices];
+  int sms = 0;
+  const int d = current_device(&sms);
+  if (d < 0) return MOE_ERR_CUDA;
+  if (sms < 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+  auto kernel = moe_tile_gemm_kernel<Mode, PMn, QMn, Epi, T>;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[2];
+  cfg.blockDim = dim3(kTgThreads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  int c = clusters[d].load();
+  if (c == 0) {
+    const int most = (int)tg_smem_bytes(1, kTgSmemTiles);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    cfg.gridDim = dim3(2 * (sms / 2));
+    cfg.dynamicSmemBytes = most;
+    if (cudaOccupancyMaxActiveClusters(&c, kernel, &cfg) != cudaSuccess || c < 1) return MOE_ERR_CUDA;
+    clusters[d].store(c);
+  }
+  size_stages(p, QMn);
+  p.pdl = pdl ? 1 : 0;
+  cfg.gridDim = dim3(2 * (unsigned)(tiles > 0 && tiles < c ? tiles : c));
+  cfg.dynamicSmemBytes = tg_smem_bytes(p.stages, p.stage_bytes);
+  if (pdl) {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool operand_ok(const void* p) { return p != nullptr && aligned(p, 16); }
+bool pitch_ok(long long ld, int width) { return ld >= width && ld % 8 == 0 && ld < (1ll << 36); }
+// K and N of a product: rows of 16-byte multiples
+bool extents_ok(int K, int N) { return K >= 8 && N >= 8 && K % 8 == 0 && N % 8 == 0; }
+bool half_type(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16; }
+
+int clear_error_word(int32_t* err, cudaStream_t st) {
+  if (err != nullptr && cudaMemsetAsync(err, 0, sizeof(int32_t), st) != cudaSuccess) return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+// N tile of a dense product of `rows` N-side rows and mt M tiles on `pairs` CTA
+// pairs: the multiple of 32 with the least (rounds of tiles) x (columns of a
+// tile + 32), the 32 standing for what a tile costs beside its MMAs.
+int pick_tile(long long rows, int mt, int batch, int pairs) {
+  int best = 256;
+  long long least = -1;
+  for (int nt = 256; nt >= 32; nt -= 32) {
+    const long long tiles = (rows + nt - 1) / nt;
+    const long long each = ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+    const long long cost = (tiles * mt * batch + pairs - 1) / pairs * (each + 32);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = (int)each;
+    }
+  }
+  return best;
+}
+
+// N tile of a ragged product: twice the mean rows of a group, so that most
+// groups are one tile and the stages of a launch with few rows are small.
+int ragged_tile(int rows, int groups) {
+  const int mean = (rows + groups - 1) / groups;
+  return mean <= 16 ? 32 : mean <= 32 ? 64 : mean <= 64 ? 128 : 256;
+}
+
+template <bool PMn>
+int launch_rows(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
+  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedN, PMn, false, kTgStore, __half>(p, tiles, false, st)
+                                 : launch<kTgRaggedN, PMn, false, kTgStore, bf16>(p, tiles, false, st);
+}
+
+int launch_wgrad(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
+  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedK, true, true, kTgStore, __half>(p, tiles, false, st)
+                                 : launch<kTgRaggedK, true, true, kTgStore, bf16>(p, tiles, false, st);
+}
+
+// y = x W (transpose: x W^T) for one or several row groups; epilogue fields of p set by the caller.
+int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int rows, int groups, int K, int N,
+                 bool transpose, int dtype, void* y, long long ldy, cudaStream_t st) {
+  int sms = 0;
+  if (current_device(&sms) < 0) return MOE_ERR_CUDA;
+  p.M = N;
+  p.N = rows;
+  p.K = K;
+  p.groups = groups;
+  p.f16 = dtype == MOE_DTYPE_FP16;
+  p.out = y;
+  p.ldo = ldy;
+  const int mt = (N + 255) / 256;
+  long long tiles = 0;
+  if (p.offsets == nullptr) {
+    p.nt = pick_tile(rows, mt, 1, std::max(1, sms / 2));
+    tiles = (long long)((rows + p.nt - 1) / p.nt) * mt;
+  } else {
+    p.nt = ragged_tile(rows, groups);
+  }
+  if (((long long)rows / 32 + groups) * mt >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const Operand P = transpose ? Operand{W, (uint64_t)K, (uint64_t)N, (uint64_t)K, (uint64_t)groups, (uint64_t)K * N}
+                              : Operand{W, (uint64_t)N, (uint64_t)K, (uint64_t)N, (uint64_t)groups, (uint64_t)K * N};
+  const Operand Q{x, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 1, 0};
+  if (!set_maps(p, P, !transpose, Q, false)) return MOE_ERR_CUDA;
+  return transpose ? launch_rows<false>(p, dtype, tiles, st) : launch_rows<true>(p, dtype, tiles, st);
+}
+
+// dW[g] = x_g^T dy_g
+int weight_gradient(TgParams& p, const void* x, long long ldx, const void* dy, long long lddy, int rows, int groups,
+                    int K, int N, int dtype, void* dW, cudaStream_t st) {
+  int sms = 0;
+  if (current_device(&sms) < 0) return MOE_ERR_CUDA;
+  p.M = N;
+  p.N = K;
+  p.K = rows;
+  p.groups = groups;
+  p.f16 = dtype == MOE_DTYPE_FP16;
+  p.out = dW;
+  p.ldo = N;
+  p.out_bs = (long long)K * N;
+  const int mt = (N + 255) / 256;
+  p.nt = pick_tile(K, mt, groups, std::max(1, sms / 2));
+  const long long tiles = (long long)((K + p.nt - 1) / p.nt) * mt * groups;
+  if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const Operand P{dy, (uint64_t)N, (uint64_t)rows, (uint64_t)lddy, 1, 0};
+  const Operand Q{x, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 1, 0};
+  if (!set_maps(p, P, true, Q, true)) return MOE_ERR_CUDA;
+  return launch_wgrad(p, dtype, tiles, st);
+}
+
+size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// ---- linear_backward workspace: dz [T, N] and the bias gradient's partial sums
+int bias_chunks(int T) { return std::min(128, (T + kActRows - 1) / kActRows); }
+size_t dz_bytes(int T, int N) { return up((size_t)T * N * 2, 256); }
+
+// ---- orthogonalize workspace
+struct OrthoLayout {
+  size_t x[2], lo, a, b, partial, alpha, total;
+  long long ldx, lda, bsx, bsa;
+};
+OrthoLayout ortho_layout(int batch, int m, int n) {
+  OrthoLayout L{};
+  const int p = std::min(m, n);
+  L.ldx = (long long)up(n, 64);
+  L.lda = (long long)up(p, 64);
+  L.bsx = L.ldx * m;
+  L.bsa = L.lda * p;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up(bytes, 256);
+    return at;
+  };
+  L.x[0] = take((size_t)batch * L.bsx * 2);
+  L.x[1] = take((size_t)batch * L.bsx * 2);
+  L.lo = take((size_t)batch * L.bsx * 2);
+  L.a = take((size_t)batch * L.bsa * 2);
+  L.b = take((size_t)batch * L.bsa * 2);
+  L.partial = take((size_t)batch * kOrthoChunks * 8);
+  L.alpha = take((size_t)batch * 4);
+  L.total = o;
+  return L;
+}
+
+}  // namespace
+
+extern "C" int moe_grouped_matmul(const void* x, long long ldx, const void* W, const int32_t* offsets, int rows,
+                                  int groups, int K, int N, int transpose, int dtype, void* y, long long ldy,
+                                  int32_t* error_word, void* stream) {
+  if (rows < 0 || groups < 1 || !half_type(dtype) || !aligned(error_word, 4)) return MOE_ERR_INVALID_ARG;
+  if (!extents_ok(K, N) || groups > kTgMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!pitch_ok(ldx, K) || !pitch_ok(ldy, N)) return MOE_ERR_INVALID_ARG;
+  if (offsets == nullptr || !aligned(offsets, 4) || !operand_ok(W)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!operand_ok(x) || !operand_ok(y))) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (int rc = clear_error_word(error_word, st)) return rc;
+  if (rows == 0) return MOE_OK;
+  TgParams p{};
+  p.offsets = offsets;
+  p.err = error_word;
+  return rows_product(p, x, ldx, W, rows, groups, K, N, transpose != 0, dtype, y, ldy, st);
+}
+
+extern "C" int moe_grouped_matmul_wgrad(const void* x, long long ldx, const void* dy, long long lddy,
+                                        const int32_t* offsets, int rows, int groups, int K, int N, int dtype, void* dW,
+                                        int32_t* error_word, void* stream) {
+  if (rows < 0 || groups < 1 || !half_type(dtype) || !aligned(error_word, 4)) return MOE_ERR_INVALID_ARG;
+  if (!extents_ok(K, N) || groups > kTgMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!pitch_ok(ldx, K) || !pitch_ok(lddy, N)) return MOE_ERR_INVALID_ARG;
+  if (offsets == nullptr || !aligned(offsets, 4) || !operand_ok(dW)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!operand_ok(x) || !operand_ok(dy))) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (int rc = clear_error_word(error_word, st)) return rc;
+  if (rows == 0)
+    return cudaMemsetAsync(dW, 0, (size_t)groups * K * N * 2, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  TgParams p{};
+  p.offsets = offsets;
+  p.err = error_word;
+  return weight_gradient(p, x, ldx, dy, lddy, rows, groups, K, N, dtype, dW, st);
+}
+
+extern "C" int moe_linear(const void* x, long long ldx, const void* W, const void* bias, const void* residual,
+                          long long ldr, int T, int K, int N, int activation, int dtype, void* y, long long ldy,
+                          void* preact, long long ldz, int32_t* error_word, void* stream) {
+  if (T < 0 || !half_type(dtype) || activation < MOE_ACT_NONE || activation > MOE_ACT_SILU || !aligned(error_word, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (!extents_ok(K, N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!pitch_ok(ldx, K) || !pitch_ok(ldy, N)) return MOE_ERR_INVALID_ARG;
+  if (!operand_ok(W) || !aligned(bias, 16)) return MOE_ERR_INVALID_ARG;
+  if (residual != nullptr && (!aligned(residual, 16) || !pitch_ok(ldr, N))) return MOE_ERR_INVALID_ARG;
+  if (preact != nullptr && (!aligned(preact, 16) || !pitch_ok(ldz, N))) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!operand_ok(x) || !operand_ok(y))) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (int rc = clear_error_word(error_word, st)) return rc;
+  if (T == 0) return MOE_OK;
+  TgParams p{};
+  p.err = error_word;
+  p.bias = bias;
+  p.res = residual;
+  p.ldr = ldr;
+  p.z = preact;
+  p.ldz = ldz;
+  p.act = activation;
+  return rows_product(p, x, ldx, W, T, 1, K, N, false, dtype, y, ldy, st);
+}
+
+extern "C" size_t moe_linear_backward_workspace_bytes(int T, int N, int activation, int bias_grad) {
+  if (T < 1 || N < 1) return 0;
+  return (activation != MOE_ACT_NONE ? dz_bytes(T, N) : 0) + (bias_grad ? (size_t)bias_chunks(T) * N * 4 : 0);
+}
+
+extern "C" int moe_linear_backward(const void* dy, long long lddy, const void* x, long long ldx, const void* W,
+                                   const void* preact, long long ldz, int T, int K, int N, int activation, int dtype,
+                                   void* dx, long long lddx, void* dW, void* dbias, void* workspace,
+                                   size_t workspace_bytes, int32_t* error_word, void* stream) {
+  if (T < 0 || !half_type(dtype) || activation < MOE_ACT_NONE || activation > MOE_ACT_SILU || !aligned(error_word, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (!extents_ok(K, N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const bool act = activation != MOE_ACT_NONE;
+  if (!pitch_ok(lddy, N) || (act && !pitch_ok(ldz, N))) return MOE_ERR_INVALID_ARG;
+  if (dx != nullptr && (!pitch_ok(lddx, K) || !aligned(dx, 16) || !operand_ok(W))) return MOE_ERR_INVALID_ARG;
+  if (dW != nullptr && (!pitch_ok(ldx, K) || !aligned(dW, 16))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dbias, 16)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!operand_ok(dy) || (act && !operand_ok(preact)) || (dW != nullptr && !operand_ok(x))))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_linear_backward_workspace_bytes(T, N, activation, dbias != nullptr);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (int rc = clear_error_word(error_word, st)) return rc;
+  if (T == 0) {
+    if (dW != nullptr && cudaMemsetAsync(dW, 0, (size_t)K * N * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias != nullptr && cudaMemsetAsync(dbias, 0, (size_t)N * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  void* dz = act ? workspace : const_cast<void*>(dy);
+  const long long lddz = act ? N : lddy;
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (act ? dz_bytes(T, N) : 0));
+  if (act || dbias != nullptr) {
+    const int chunks = bias_chunks(T);
+    ActParams a{dy, lddy, preact, ldz, act ? dz : nullptr, dbias ? partial : nullptr, dbias, T, N,
+                (T + chunks - 1) / chunks, chunks, activation};
+    const dim3 grid((N + kActCols - 1) / kActCols, chunks);
+    if (dtype == MOE_DTYPE_FP16) moe_act_backward_kernel<__half><<<grid, 256, 0, st>>>(a);
+    else moe_act_backward_kernel<bf16><<<grid, 256, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias != nullptr) {
+      if (dtype == MOE_DTYPE_FP16) moe_bias_sum_kernel<__half><<<(N + 255) / 256, 256, 0, st>>>(a);
+      else moe_bias_sum_kernel<bf16><<<(N + 255) / 256, 256, 0, st>>>(a);
+      if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    }
+  }
+  if (dx != nullptr) {
+    TgParams p{};
+    p.err = error_word;
+    if (int rc = rows_product(p, dz, lddz, W, T, 1, N, K, true, dtype, dx, lddx, st)) return rc;
+  }
+  if (dW != nullptr) {
+    TgParams p{};
+    p.err = error_word;
+    if (int rc = weight_gradient(p, x, ldx, dz, lddz, T, 1, K, N, dtype, dW, st)) return rc;
+  }
+  return MOE_OK;
+}
+
+extern "C" size_t moe_orthogonalize_workspace_bytes(int batch, int m, int n) {
+  return batch < 1 || m < 1 || n < 1 ? 0 : ortho_layout(batch, m, n).total;
+}
+
+extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, int batch, int m, int n, int dtype,
+                                 int steps, const float* coeffs, float eps, void* out, long long ldo, long long bso,
+                                 void* workspace, size_t workspace_bytes, int32_t* error_word, void* stream) {
+  const int elem = dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (batch < 0 || m < 1 || n < 1 || (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP32) || coeffs == nullptr ||
+      !(eps >= 0.f) || !aligned(error_word, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (steps < 1 || steps > 64 || std::max(m, n) > (1 << 16) || batch > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (ldg < n || ldo < n || (batch > 1 && (bsg < ldg * (m - 1) + n || bso < ldo * (m - 1) + n)))
+    return MOE_ERR_INVALID_ARG;
+  if (batch > 0 && (G == nullptr || out == nullptr || !aligned(G, elem) || !aligned(out, 2))) return MOE_ERR_INVALID_ARG;
+  const OrthoLayout L = ortho_layout(std::max(batch, 1), m, n);
+  if (batch > 0 && (workspace == nullptr || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
+  if (batch > 0 && workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (int rc = clear_error_word(error_word, st)) return rc;
+  if (batch == 0) return MOE_OK;
+  int sms = 0;
+  if (current_device(&sms) < 0) return MOE_ERR_CUDA;
+  const int pairs = std::max(1, sms / 2);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const bool tall = m > n;
+  const int p0 = std::min(m, n), q0 = std::max(m, n);
+  // X is stored times 2^s with s = log2(sqrt(q)) (floored): entries of an orthogonal p x q matrix are near
+  // 1 / sqrt(q), those of the normalised gradient near 1 / sqrt(p q), both normal fp16 numbers after it.
+  int s = 0;
+  while ((1ll << (2 * (s + 1))) <= q0) ++s;
+  const float xs = (float)(1 << s), as = 1024.f;   // A and B are stored times 2^10
+
+  OrthoParams o{G, ldg, bsg, m, n, xs, eps, reinterpret_cast<double*>(ws + L.partial),
+                reinterpret_cast<float*>(ws + L.alpha), reinterpret_cast<__half*>(ws + L.x[0]),
+                reinterpret_cast<__half*>(ws + L.lo), L.ldx, L.bsx,
+                (int)std::min<long long>(kOrthoChunks, ((long long)m * n + 8191) / 8192)};
+  const dim3 grid(o.chunks, batch);
+  if (dtype == MOE_DTYPE_FP32) {
+    moe_ortho_norm_kernel<float><<<grid, 256, 0, st>>>(o);
+    moe_ortho_scale_kernel<float><<<grid, 256, 0, st>>>(o);
+  } else {
+    moe_ortho_norm_kernel<bf16><<<grid, 256, 0, st>>>(o);
+    moe_ortho_scale_kernel<bf16><<<grid, 256, 0, st>>>(o);
+  }
+  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+
+  const Operand A{ws + L.a, (uint64_t)p0, (uint64_t)p0, (uint64_t)L.lda, (uint64_t)batch, (uint64_t)L.bsa};
+  const Operand B{ws + L.b, (uint64_t)p0, (uint64_t)p0, (uint64_t)L.lda, (uint64_t)batch, (uint64_t)L.bsa};
+  for (int i = 0; i < steps; ++i) {
+    const Operand X{ws + L.x[i & 1], (uint64_t)n, (uint64_t)m, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
+    const float a = coeffs[3 * i], b = coeffs[3 * i + 1], c = coeffs[3 * i + 2];
+    const float* alpha = i == 0 ? o.alpha : nullptr;
+    const int mt = (p0 + 255) / 256;
+    const long long tri = (long long)batch * mt * (mt + 1) / 2;
+    TgParams g{};
+    g.err = error_word;
+    g.f16 = 1;
+    g.groups = batch;
+    g.M = g.N = p0;
+    g.nt = 256;
+    g.ldo = g.ldi = L.lda;
+    g.out_bs = g.in_bs = L.bsa;
+    // A = X X^T (X^T X for a tall X)
+    TgParams g1 = g;
+    g1.K = q0;
+    g1.out = ws + L.a;
+    g1.alpha = alpha;
+    g1.cb = as / (xs * xs);
+    if (!set_maps(g1, X, tall, X, tall)) return MOE_ERR_CUDA;
+    int rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(g1, tri, true, st)
+                  : launch<kTgSymmetric, false, false, kTgGram, __half>(g1, tri, true, st);
+    if (rc) return rc;
+    // B = b A + c A A
+    TgParams g2 = g;
+    g2.K = p0;
+    g2.out = ws + L.b;
+    g2.in = reinterpret_cast<const __half*>(ws + L.a);
+    g2.ca = b;
+    g2.cb = c / as;
+    if (!set_maps(g2, A, false, A, false)) return MOE_ERR_CUDA;
+    if ((rc = launch<kTgSymmetric, false, false, kTgPoly, __half>(g2, tri, true, st))) return rc;
+    // X' = a X + B X: rows of X on the N side, its columns on the M side
+    TgParams g3 = g;
+    const bool last = i == steps - 1;
+    g3.M = n;
+    g3.N = m;
+    g3.K = p0;
+    g3.nt = pick_tile(m, (n + 255) / 256, batch, pairs);
+    g3.in = reinterpret_cast<const __half*>(ws + L.x[i & 1]);
+    g3.lo = reinterpret_cast<__half*>(ws + L.lo);
+    g3.ldi = L.ldx;
+    g3.in_bs = L.bsx;
+    g3.alpha = alpha;
+    const float back = last ? 1.f / xs : 1.f;
+    g3.ca = a * back;
+    g3.cb = back / as;
+    g3.out = last ? out : ws + L.x[(i + 1) & 1];
+    g3.ldo = last ? ldo : L.ldx;
+    g3.out_bs = last ? bso : L.bsx;
+    // wide: X'[r, c] = sum_k X[k, c] B[r, k];  tall: X'[r, c] = sum_k B[c, k] X[r, k]  (B symmetric)
+    if (!(tall ? set_maps(g3, B, false, X, false) : set_maps(g3, X, true, B, false))) return MOE_ERR_CUDA;
+    const long long tiles = (long long)((m + g3.nt - 1) / g3.nt) * ((n + 255) / 256) * batch;
+    if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (tall)
+      rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(g3, tiles, true, st)
+                : launch<kTgBatched, false, false, kTgUpdate, __half>(g3, tiles, true, st);
+    else
+      rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(g3, tiles, true, st)
+                : launch<kTgBatched, true, false, kTgUpdate, __half>(g3, tiles, true, st);
+    if (rc) return rc;
+  }
+  return MOE_OK;
+}

@@ -1,0 +1,243 @@
+// Element passes of the operators around the MoE layer: the activation's
+// backward with the bias gradient's sums, and the normalisation that opens the
+// Newton-Schulz iteration. All are one read and one write of their tensors,
+// bound by HBM; sums are fp32 (fp64 for the norm) in a fixed order.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "common.cuh"
+#include "tile_gemm.cuh"
+
+namespace moe {
+
+constexpr int kActCols = 256;   // columns of a block: 32 lanes x 8
+constexpr int kActRows = 32;    // least rows of a block's chunk
+constexpr int kOrthoChunks = 256;
+
+struct ActParams {
+  const void* dy;
+  long long lddy;
+  const void* z;
+  long long ldz;
+  void* dz;          // [T, N], or null (no activation: dz is dy)
+  float* partial;    // [chunks, N], or null
+  void* dbias;       // [N]
+  int T, N, rows, chunks, act;
+};
+
+// d act(z) / dz
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? 1.f : 0.f;
+    case kActGelu:
+      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    case kActGeluTanh: {
+      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
+      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+    }
+    case kActSilu: {
+      const float q = 1.f / (1.f + expf(-z));
+      return q * (1.f + z * (1.f - q));
+    }
+    default: return 1.f;
+  }
+}
+
+// dz = dy act'(z), rounded once to the operand type of the two products that
+// read it, and this chunk's column sums of the unrounded dz.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_act_backward_kernel(const ActParams p) {
+  __shared__ float sums[8][kActCols];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int col = blockIdx.x * kActCols + tx * 8;
+  const int r0 = blockIdx.y * p.rows, r1 = min(p.T, r0 + p.rows);
+  float acc[8] = {};
+  if (col < p.N) {   // N is a multiple of 8
+    const T* dy = reinterpret_cast<const T*>(p.dy);
+    const T* z = reinterpret_cast<const T*>(p.z);
+    T* dz = reinterpret_cast<T*>(p.dz);
+#pragma unroll 2
+    for (int r = r0 + ty; r < r1; r += 8) {
+      const uint4 g = *reinterpret_cast<const uint4*>(dy + (long long)r * p.lddy + col);
+      uint4 v = g;
+      if (p.act != kActNone) v = *reinterpret_cast<const uint4*>(z + (long long)r * p.ldz + col);
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, zw[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 d = TgPair<T>::unpack(gw[i]);
+        if (p.act != kActNone) {
+          const float2 zf = TgPair<T>::unpack(zw[i]);
+          d.x *= act_slope(zf.x, p.act);
+          d.y *= act_slope(zf.y, p.act);
+        }
+        acc[2 * i] += d.x;
+        acc[2 * i + 1] += d.y;
+        o[i] = TgPair<T>::pack(d.x, d.y);
+      }
+      if (p.dz != nullptr)
+        *reinterpret_cast<uint4*>(dz + (long long)r * p.N + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (p.partial == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[ty][tx * 8 + i] = acc[i];
+  __syncthreads();
+  const int c = blockIdx.x * kActCols + threadIdx.x;
+  if (c < p.N) {
+    float v = 0.f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) v += sums[y][threadIdx.x];
+    p.partial[(long long)blockIdx.y * p.N + c] = v;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) moe_bias_sum_kernel(const ActParams p) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.N) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < p.chunks; ++i) v += p.partial[(long long)i * p.N + c];
+  reinterpret_cast<T*>(p.dbias)[c] = T(v);
+}
+
+// ---------------------------------------------------------------- orthogonalize
+struct OrthoParams {
+  const void* g;
+  long long ldg, bsg;
+  int m, n;
+  float xs, eps;
+  double* partial;   // [batch, kOrthoChunks]
+  float* alpha;      // [batch]
+  __half* hi;
+  __half* lo;
+  long long ldx, bsx;
+  int chunks;
+};
+
+template <typename T>
+__device__ __forceinline__ float ortho_value(const T* p) { return (float)*p; }
+
+// Threads of a block along a row (the rest along rows): enough for the row, 32 at least.
+__device__ __forceinline__ int ortho_lanes(int items) { return items > 128 ? 256 : items > 64 ? 128 : items > 32 ? 64 : 32; }
+
+template <typename F>
+__device__ __forceinline__ double block_sum(double v, F* scratch) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += scratch[i];
+  return s;
+}
+
+// Eight elements where every row starts on 16 bytes, else one at a time.
+template <typename T>
+__device__ __forceinline__ bool ortho_wide(const OrthoParams& p) {
+  return p.n % 8 == 0 && p.ldg % 8 == 0 && p.bsg % 8 == 0 && (reinterpret_cast<uintptr_t>(p.g) & 15) == 0;
+}
+template <typename T>
+__device__ __forceinline__ void ortho_load8(const T* p, float (&v)[8]) {
+  if (sizeof(T) == 4) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = TgPair<bf16>::unpack(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// Squares summed in fp64: neither a large fp32 gradient overflows nor a small one vanishes.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_ortho_norm_kernel(const OrthoParams p) {
+  __shared__ double scratch[8];
+  const T* g = reinterpret_cast<const T*>(p.g) + blockIdx.y * p.bsg;
+  const bool wide = ortho_wide<T>(p);
+  const int items = wide ? p.n / 8 : p.n;
+  const int lanes = ortho_lanes(items);
+  const int tx = threadIdx.x & (lanes - 1), ty = threadIdx.x / lanes, rows = 256 / lanes;
+  double acc = 0;
+  for (int r = blockIdx.x * rows + ty; r < p.m; r += gridDim.x * rows) {
+    const T* row = g + (long long)r * p.ldg;
+    if (wide) {
+#pragma unroll 4
+      for (int c = tx; c < items; c += lanes) {
+        float v[8];
+        ortho_load8(row + c * 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc += (double)v[i] * v[i];
+      }
+    } else {
+#pragma unroll 4
+      for (int c = tx; c < items; c += lanes) {
+        const double v = ortho_value(row + c);
+        acc += v * v;
+      }
+    }
+  }
+  const double s = block_sum(acc, scratch);
+  if (threadIdx.x == 0) p.partial[blockIdx.y * kOrthoChunks + blockIdx.x] = s;
+}
+
+// X0 = G / (|G| + eps) as two factors: G times a power of two, exact up to the
+// width of the fp16 pair (upper half hi, remainder lo: 22 bits), and
+// alpha = 2^E / (|G| + eps), which the first step's epilogues apply in fp32.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_ortho_scale_kernel(const OrthoParams p) {
+  __shared__ double scratch[8];
+  const double total =
+      block_sum(threadIdx.x < p.chunks ? p.partial[blockIdx.y * kOrthoChunks + threadIdx.x] : 0.0, scratch);
+  const double norm = sqrt(total);
+  const int e = norm > 0 && norm < 1e300 ? ilogb(norm) : 0;
+  const double scale = ldexp((double)p.xs, -e);
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    p.alpha[blockIdx.y] = norm > 0 ? (float)(ldexp(1.0, e) / (norm + p.eps)) : norm == 0 ? 0.f : (float)norm;
+  const T* g = reinterpret_cast<const T*>(p.g) + blockIdx.y * p.bsg;
+  __half* hi = p.hi + blockIdx.y * p.bsx;
+  __half* lo = p.lo + blockIdx.y * p.bsx;
+  const bool wide = ortho_wide<T>(p);
+  const int items = wide ? p.n / 8 : p.n;
+  const int lanes = ortho_lanes(items);
+  const int tx = threadIdx.x & (lanes - 1), ty = threadIdx.x / lanes, rows = 256 / lanes;
+  for (int r = blockIdx.x * rows + ty; r < p.m; r += gridDim.x * rows) {
+    const T* row = g + (long long)r * p.ldg;
+    if (wide) {
+#pragma unroll 2
+      for (int c = tx; c < items; c += lanes) {
+        float v[8];
+        ortho_load8(row + c * 8, v);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = (float)(v[2 * i] * scale), b = (float)(v[2 * i + 1] * scale);
+          h[i] = TgPair<__half>::pack(a, b);
+          const float2 f = TgPair<__half>::unpack(h[i]);
+          l[i] = TgPair<__half>::pack(a - f.x, b - f.y);
+        }
+        *reinterpret_cast<uint4*>(hi + (long long)r * p.ldx + c * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + (long long)r * p.ldx + c * 8) = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+    } else {
+#pragma unroll 4
+      for (int c = tx; c < items; c += lanes) {
+        const float a = (float)(ortho_value(row + c) * scale);
+        const __half h = __float2half_rn(a);
+        hi[(long long)r * p.ldx + c] = h;
+        lo[(long long)r * p.ldx + c] = __float2half_rn(a - __half2float(h));
+      }
+    }
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,700 @@
+// Tiled matrix products on CTA pairs (tcgen05 cta_group::2) for the operators
+// around the MoE layer: products grouped by expert over ragged row groups, the
+// dense layer, the weight gradients of both, and the symmetric products of the
+// Newton-Schulz iteration.
+//
+// Every product is written as  out[n, m] = sum_k P[m, k] * Q[n, k]  with m
+// contiguous in the output. P, the M side, fills the 256 rows of a pair's MMA
+// (128 in each CTA); Q, the N side, its 32 .. 256 columns. For a layer's
+// forward P is W^T (so the tile's 256 rows are output features) and Q the
+// token rows: a group of c tokens then costs ceil(c / 32) * 32 columns of MMA
+// instead of whole 256-row tiles, and a weight tile is read once for up to 256
+// tokens. Either operand may have its k index contiguous ("K-major") or its m
+// / n index contiguous ("MN-major"); the tensor core reads both, so no operand
+// is ever transposed in memory.
+//
+// Roles per CTA: warp 0 TMA loads, warp 1 MMA issue (leader CTA), warp 2 the
+// zero rows of a ragged reduction's last block, warp 3 TMEM, warps 4..11 the
+// epilogue. Each CTA loads its 128 rows of P and half of the tile's Q into its
+// own shared memory; both CTAs' bytes are counted on the leader's barrier.
+// Two TMEM accumulators let a tile's epilogue run under the next tile's MMAs.
+// Tiles are dealt round robin; nothing is exchanged between pairs.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kTgThreads = 384;
+constexpr int kTgEpiWarps = 8;
+constexpr int kTgMaxStages = 12;
+constexpr int kTgMaxGroups = 1024;
+constexpr int kTgABytes = 128 * 128;     // 128 rows of P, 64 k each
+constexpr int kTgSmemTiles = 200 * 1024; // stages fill at most this
+constexpr unsigned long long kTgTimeoutNs = 2000000000ull;
+
+enum TgMode : int {
+  kTgRaggedN = 0,    // groups of N-side rows, one P per group (offsets == null: one group of all rows)
+  kTgRaggedK = 1,    // groups of the reduction, one output per group (offsets == null: one group)
+  kTgBatched = 2,    // the same product for every batch index
+  kTgSymmetric = 3,  // batched, P = Q: only the tiles on and below the diagonal, stored twice
+};
+
+enum TgEpilogue : int {
+  kTgStore = 0,     // act(acc + bias) + residual, the pre-activation kept on request
+  kTgGram = 1,      // Newton-Schulz: A = X X^T, scaled
+  kTgPoly = 2,      // B = b A + c A A
+  kTgUpdate = 3,    // X' = a X + B X (X as a pair of fp16 values)
+  kTgUpdateOut = 4, // the same, stored as bf16 at the caller's place
+};
+
+enum TgAct : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+struct TgParams {
+  CUtensorMap tm_p;      // K-major: {k, m, batch} box {64, 128}; MN-major: {m, k, batch} box {64, 64}
+  CUtensorMap tm_q[4];   // K-major: {k, n, batch} boxes of 128, 64, 32, 16 rows; MN-major: [0] box {64, 64}
+  int M, N, K;           // extents (N: rows of Q in a ragged-N product; K: rows in a ragged-K one)
+  int groups;            // groups or batches
+  int nt;                // largest N tile: 32, 64, 128 or 256
+  int stages, stage_bytes;
+  int f16;               // operands are fp16 (else bf16)
+  const int32_t* offsets;   // [groups + 1] device, or null
+  int32_t* err;             // device error word, or null
+  // output
+  void* out;
+  long long ldo, out_bs;    // row and batch pitch in elements
+  // kTgStore
+  const void* bias;         // [M]
+  const void* res;
+  long long ldr;
+  void* z;
+  long long ldz;
+  int act;
+  // Newton-Schulz
+  const __half* in;         // kTgPoly: A; kTgUpdate: X, upper half
+  __half* lo;               // kTgUpdate: X, lower half (read, then written)
+  long long ldi, in_bs;
+  const float* alpha;       // [batches]: the first step's normalisation, or null
+  float ca, cb;             // coefficients on the stored value and on the accumulator
+  int pdl;                  // launched with programmatic stream serialisation
+};
+
+struct TgSmem {
+  uint64_t full[kTgMaxStages];
+  uint64_t empty[kTgMaxStages];
+  uint64_t tail[kTgMaxStages];
+  uint64_t peer_tail[kTgMaxStages];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint32_t tmem_base;
+  int abort;
+  int total;
+  int start[kTgMaxGroups + 1];   // group offsets as used (an invalid group is empty)
+  int count[kTgMaxGroups];
+  int tile0[kTgMaxGroups + 1];   // first N tile of each group (ragged N)
+};
+
+constexpr size_t tg_smem_bytes(int stages, int stage_bytes) {
+  return 1024 + (size_t)stages * stage_bytes + sizeof(TgSmem);
+}
+
+struct TgTask {
+  int g;        // group or batch
+  int m0;       // first M row of the tile
+  int n0;       // first N row of the tile (within Q; absolute in a ragged-N product)
+  int cols;     // valid N rows
+  int nt;       // MMA columns (multiple of 32)
+  int k0, klen; // reduction range
+};
+
+__device__ __forceinline__ void tg_set_error(const TgParams& p, TgSmem& s, int code, bool stop) {
+  if (p.err != nullptr) atomicCAS(p.err, 0, code);
+  if (stop) *reinterpret_cast<volatile int*>(&s.abort) = 1;
+}
+
+// Bounded wait of one thread on a local barrier phase.
+__device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, const TgParams& p, TgSmem& s) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
+    if (ptx::globaltimer() - t0 > kTgTimeoutNs) {
+      tg_set_error(p, s, kDevTimeout, true);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Position of tile `idx` in a grid of mt x ntl tiles: bands of 8 M tiles, all
+// N tiles of a band before the next band, so that the pairs working at one
+// time share both operands in L2 (74 pairs cover about 8 x 9 tiles).
+__device__ __forceinline__ void tg_raster(int idx, int mt, int ntl, int& m, int& n) {
+  constexpr int kBand = 8;
+  const int band = idx / (kBand * ntl);
+  const int wide = min(kBand, mt - band * kBand);
+  const int rem = idx - band * kBand * ntl;
+  n = rem / wide;
+  m = band * kBand + rem - n * wide;
+}
+
+// N tile j of `rows` rows: equal tiles of a multiple of 32 rows, at most cap
+// (their number is the smallest possible, so none is empty).
+__device__ __forceinline__ void tg_split(int rows, int cap, int j, int& at, int& cols) {
+  const int tiles = (rows + cap - 1) / cap;
+  const int each = ((rows + tiles - 1) / tiles + 31) & ~31;
+  at = j * each;
+  cols = min(each, rows - at);
+}
+
+template <int Mode>
+__device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, const TgSmem& s) {
+  TgTask k{};
+  const int mt = (p.M + 255) >> 8;
+  if (Mode == kTgRaggedN) {
+    int lo = 0, hi = p.groups - 1;   // the last group whose first tile is at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.tile0[mid] * mt <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    k.g = lo;
+    const int ntl = s.tile0[lo + 1] - s.tile0[lo];
+    int m, n;
+    tg_raster(t - s.tile0[lo] * mt, mt, ntl, m, n);
+    tg_split(s.count[lo], p.nt, n, k.n0, k.cols);
+    k.n0 += s.start[lo];
+    k.m0 = m << 8;
+    k.k0 = 0;
+    k.klen = p.K;
+  } else if (Mode == kTgSymmetric) {
+    const int per = mt * (mt + 1) / 2;
+    k.g = t / per;
+    int r = t - k.g * per, m = 0;
+    while (r > m) r -= ++m;          // row m of the triangle has m + 1 tiles
+    k.m0 = m << 8;
+    k.n0 = r << 8;
+    k.cols = min(256, p.N - k.n0);
+    k.klen = p.K;
+  } else {
+    const int ntl = (p.N + p.nt - 1) / p.nt;
+    k.g = t / (mt * ntl);
+    int m, n;
+    tg_raster(t - k.g * mt * ntl, mt, ntl, m, n);
+    tg_split(p.N, p.nt, n, k.n0, k.cols);
+    k.m0 = m << 8;
+    if (Mode == kTgRaggedK) {
+      k.k0 = s.start[k.g];
+      k.klen = s.count[k.g];
+    } else {
+      k.klen = p.K;
+    }
+  }
+  k.nt = (k.cols + 31) & ~31;
+  return k;
+}
+
+// Reduction steps (of 16) of k block kb.
+__device__ __forceinline__ int tg_ksteps(const TgTask& k, int kb) { return min(4, (k.klen - kb * 64 + 15) >> 4); }
+
+// ---------------------------------------------------------------- loads
+__device__ __forceinline__ void tg_load3(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// This CTA's half of one stage; returns nothing, all bytes are counted on `bar`.
+template <bool PMn, bool QMn>
+__device__ __forceinline__ void tg_load_stage(uint32_t dst, const TgParams& p, const TgTask& k, int kpos, int rank,
+                                              uint32_t bar, int pbatch, int qbatch) {
+  const int m = k.m0 + rank * 128;
+  if (PMn) {
+    tg_load3(dst, &p.tm_p, bar, m, kpos, pbatch);
+    tg_load3(dst + 8192, &p.tm_p, bar, m + 64, kpos, pbatch);
+  } else {
+    tg_load3(dst, &p.tm_p, bar, kpos, m, pbatch);
+  }
+  const uint32_t q = dst + kTgABytes;
+  const int half = k.nt >> 1;
+  const int n = k.n0 + rank * half;
+  if (QMn) {
+    for (int j = 0; j < half; j += 64) tg_load3(q + j * 128, &p.tm_q[0], bar, n + j, kpos, qbatch);
+  } else {
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // half = a sum of boxes of 128, 64, 32 and 16 rows
+      const int rows = 128 >> i;
+      if (half & rows) {
+        tg_load3(q + at * 128, &p.tm_q[i], bar, kpos, n + at, qbatch);
+        at += rows;
+      }
+    }
+  }
+}
+
+template <bool QMn>
+__device__ __forceinline__ uint32_t tg_stage_tx(const TgTask& k) {
+  const int half = k.nt >> 1;
+  return kTgABytes + (QMn ? ((half + 63) >> 6) * 8192 : half * 128);
+}
+
+template <int Mode>
+__device__ __forceinline__ bool tg_has_tail(const TgTask& k, int kb) {
+  // a ragged reduction's last block runs into the next group's rows inside a step of 16
+  return Mode == kTgRaggedK && k.klen - kb * 64 < 64 && (k.klen & 15) != 0;
+}
+
+template <int Mode, bool PMn, bool QMn>
+__device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t rank, int first, int step) {
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int t = first; t < s.total && ok; t += step) {
+    const TgTask k = tg_decode<Mode>(t, p, s);
+    const int nk = (k.klen + 63) >> 6;
+    const uint32_t tx = tg_stage_tx<QMn>(k);
+    const int pbatch = Mode == kTgRaggedK ? 0 : k.g;
+    const int qbatch = Mode == kTgRaggedK || Mode == kTgRaggedN ? 0 : k.g;
+    for (int kb = 0; kb < nk; ++kb) {
+      if (!tg_wait(&s.empty[stage], phase ^ 1, p, s)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = tiles + stage * p.stage_bytes;
+      uint32_t bar;
+      if (tg_has_tail<Mode>(k, kb)) {
+        ptx::mbar_arrive_expect_tx(&s.tail[stage], tx);
+        bar = ptx::mapa(ptx::smem_u32(&s.tail[stage]), rank);
+      } else {
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&s.full[stage], 2 * tx);
+        bar = ptx::mapa(ptx::smem_u32(&s.full[stage]), 0);
+      }
+      tg_load_stage<PMn, QMn>(dst, p, k, k.k0 + kb * 64, rank, bar, pbatch, qbatch);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  // the commits that free the stages have arrived before this CTA's barriers go away
+  for (int i = 0; ok && i < p.stages; ++i) {
+    ok = tg_wait(&s.empty[stage], phase ^ 1, p, s);
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!ok) {   // given up: let the copies in flight land before the shared memory goes away
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 5000000ull) __nanosleep(1000);
+  }
+}
+
+// ---------------------------------------------------------------- zero rows of a ragged reduction's last block
+// The block holds the group's last klen % 64 rows and then rows of the next
+// group. Steps of 16 past the group are not issued; the rows left inside the
+// last step are overwritten with zeros in both operands (zeros in one alone
+// would still meet an infinity or NaN of another group in the other).
+template <int Mode>
+__device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint32_t rank, int first, int step) {
+  if (Mode != kTgRaggedK) return;
+  const int lane = ptx::lane_id();
+  int stage = 0;
+  uint32_t used = 0;   // parity of each stage's tail barrier
+  for (int t = first; t < s.total; t += step) {
+    const TgTask k = tg_decode<Mode>(t, p, s);
+    const int nk = (k.klen + 63) >> 6;
+    if (nk == 0) continue;
+    const int last = (stage + nk - 1) % p.stages;
+    if (tg_has_tail<Mode>(k, nk - 1)) {
+      bool ok = true;
+      if (lane == 0) ok = tg_wait(&s.tail[last], (used >> last) & 1, p, s);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+      const int r0 = k.klen & 63, r1 = (r0 + 15) & ~15;
+      const int boxes = 2 + (((k.nt >> 1) + 63) >> 6);
+      uint8_t* at = tiles + (size_t)last * p.stage_bytes;
+      for (int b = 0; b < boxes; ++b)
+        for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+          *reinterpret_cast<uint4*>(at + b * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+      ptx::fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0) {
+          ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&s.peer_tail[last]), 0));
+        } else {
+          uint64_t* bar = &s.peer_tail[last];
+          const uint64_t t0 = ptx::globaltimer();
+          while (!ptx::mbar_try_wait_cluster(bar, (used >> last) & 1)) {
+            if (*reinterpret_cast<volatile int*>(&s.abort)) break;
+            if (ptx::globaltimer() - t0 > kTgTimeoutNs) {
+              tg_set_error(p, s, kDevTimeout, true);
+              break;
+            }
+          }
+          ptx::mbar_arrive(&s.full[last]);
+        }
+      }
+      __syncwarp();
+      used ^= 1u << last;
+    }
+    stage = (stage + nk) % p.stages;
+  }
+}
+
+// ---------------------------------------------------------------- MMA (leader)
+template <int Mode, bool PMn, bool QMn>
+__device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tmem, int first, int step) {
+  const uint32_t fmt = p.f16 ? 0u : 1u;
+  const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((PMn ? 1u : 0u) << 15) | ((QMn ? 1u : 0u) << 16) |
+                          ((256u >> 4) << 24);
+  int stage = 0;
+  uint32_t phase = 0;
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (int t = first; t < s.total; t += step) {
+    const TgTask k = tg_decode<Mode>(t, p, s);
+    const int nk = (k.klen + 63) >> 6;
+    if (nk == 0) continue;
+    if (!tg_wait(&s.acc_empty[acc], acc_phase ^ 1, p, s)) return;
+    ptx::tc_fence_after();
+    const uint32_t d = tmem + acc * 256;
+    const uint32_t idesc = idesc0 | ((uint32_t)(k.nt >> 3) << 17);
+    for (int kb = 0; kb < nk; ++kb) {
+      if (!tg_wait(&s.full[stage], phase, p, s)) return;
+      ptx::tc_fence_after();
+      const uint32_t a = tiles + stage * p.stage_bytes;
+      const uint32_t b = a + kTgABytes;
+      const int steps = Mode == kTgRaggedK ? tg_ksteps(k, kb) : 4;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (Mode == kTgRaggedK && kk >= steps) break;
+        const uint64_t ad = PMn ? ptx::smem_desc_sw128(a + kk * 2048, 8192, 1024)
+                                : ptx::smem_desc_sw128(a + kk * 32, 16, 1024);
+        const uint64_t bd = QMn ? ptx::smem_desc_sw128(b + kk * 2048, 8192, 1024)
+                                : ptx::smem_desc_sw128(b + kk * 32, 16, 1024);
+        ptx::mma_bf16_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+      }
+      ptx::mma_commit_pair_multicast(&s.empty[stage], 0x3);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    ptx::mma_commit_pair_multicast(&s.acc_full[acc], 0x3);
+    if (++acc == 2) {
+      acc = 0;
+      acc_phase ^= 1;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- epilogue
+template <typename T>
+struct TgPair;
+template <>
+struct TgPair<bf16> {
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+template <>
+struct TgPair<__half> {
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+__device__ __forceinline__ float tg_act(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f || z != z ? z : 0.f;
+    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case kActGeluTanh: return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+    case kActSilu: return z / (1.f + expf(-z));
+    default: return z;
+  }
+}
+
+// 32 accumulator columns of one warp: lane l holds column m (= m0 + l) of 32
+// consecutive output rows, row0 .. row0 + 31, of which nrow exist.
+//
+// Row-wise outputs: neighbouring lanes swap halves so that each holds two
+// consecutive columns of one row; a store instruction then covers two rows of
+// 64 contiguous bytes with 4 bytes per lane. What the epilogue reads (the
+// residual, X) is loaded for all 32 rows before the first use.
+template <int Epi, typename T>
+__device__ __forceinline__ void tg_emit_rows(uint32_t (&r)[32], const TgParams& p, const TgTask& k, int row0, int nrow,
+                                             int m, int lane, float2 bias, float alpha) {
+  const int odd = lane & 1;
+  const int m2 = m - odd;
+  if (m2 >= p.M) nrow = 0;   // still takes part in the swaps
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[2 * i] : r[2 * i + 1], 1);
+    if (odd) r[2 * i] = got;
+    else r[2 * i + 1] = got;
+  }
+  if (Epi == kTgStore) {
+    uint32_t v[16];
+    if (p.res != nullptr) {
+      const T* res = reinterpret_cast<const T*>(p.res) + (long long)(row0 + odd) * p.ldr + m2;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = 2 * i + odd < nrow ? *reinterpret_cast<const uint32_t*>(res + 2 * i * p.ldr) : 0u;
+    }
+    T* out = reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)(row0 + odd) * p.ldo + m2;
+    T* z = reinterpret_cast<T*>(p.z) + (long long)(row0 + odd) * p.ldz + m2;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i + odd >= nrow) break;
+      float a = __uint_as_float(r[2 * i]) + bias.x, b = __uint_as_float(r[2 * i + 1]) + bias.y;
+      if (p.z != nullptr) *reinterpret_cast<uint32_t*>(z + 2 * i * p.ldz) = TgPair<T>::pack(a, b);
+      if (p.act != kActNone) {
+        a = tg_act(a, p.act);
+        b = tg_act(b, p.act);
+      }
+      if (p.res != nullptr) {
+        const float2 f = TgPair<T>::unpack(v[i]);
+        a += f.x;
+        b += f.y;
+      }
+      *reinterpret_cast<uint32_t*>(out + 2 * i * p.ldo) = TgPair<T>::pack(a, b);
+    }
+  } else {
+    // the pair (m2, m2 + 1) lies in the padded pitch even where m2 + 1 is past the matrix
+    const long long at = k.g * p.in_bs + (long long)(row0 + odd) * p.ldi + m2;
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool in = 2 * i + odd < nrow;
+      hi[i] = in ? *reinterpret_cast<const uint32_t*>(p.in + at + 2 * i * p.ldi) : 0u;
+      lo[i] = in ? *reinterpret_cast<const uint32_t*>(p.lo + at + 2 * i * p.ldi) : 0u;
+    }
+    const float ca = alpha * p.ca, cb = alpha * p.cb;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i + odd >= nrow) break;
+      const float2 h = TgPair<__half>::unpack(hi[i]), l = TgPair<__half>::unpack(lo[i]);
+      const float a = ca * (h.x + l.x) + cb * __uint_as_float(r[2 * i]);
+      const float b = ca * (h.y + l.y) + cb * __uint_as_float(r[2 * i + 1]);
+      if (Epi == kTgUpdate) {
+        const uint32_t n = TgPair<__half>::pack(a, b);
+        const float2 nf = TgPair<__half>::unpack(n);
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<__half*>(p.out) + at + 2 * i * p.ldi) = n;
+        *reinterpret_cast<uint32_t*>(p.lo + at + 2 * i * p.ldi) = TgPair<__half>::pack(a - nf.x, b - nf.y);
+      } else {
+        bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)(row0 + 2 * i + odd) * p.ldo + m2;
+        if ((reinterpret_cast<uintptr_t>(o) & 3) == 0 && m2 + 1 < p.M) {
+          *reinterpret_cast<uint32_t*>(o) = TgPair<bf16>::pack(a, b);
+        } else {
+          o[0] = __float2bfloat16(a);
+          if (m2 + 1 < p.M) o[1] = __float2bfloat16(b);
+        }
+      }
+    }
+  }
+}
+
+// Symmetric outputs (A = X X^T and B = b A + c A A): the lane's 32 values are
+// 64 contiguous bytes of row m of the output (whose pitch is padded to 64, so
+// columns past the matrix may be written), and, off the diagonal, column m of
+// the 32 rows of the mirrored tile.
+template <int Epi>
+__device__ __forceinline__ void tg_emit_symmetric(const uint32_t (&r)[32], const TgParams& p, const TgTask& k, int row0,
+                                                  int nrow, int m, float alpha) {
+  if (m >= p.M) return;
+  __half* out = reinterpret_cast<__half*>(p.out) + k.g * p.out_bs;
+  const float cb = p.cb * alpha * alpha;
+  uint4 w[4];
+  if (Epi == kTgPoly) {
+    const uint4* in = reinterpret_cast<const uint4*>(p.in + k.g * p.in_bs + (long long)m * p.ldi + row0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = in[i];
+  }
+  uint32_t* v = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a = cb * __uint_as_float(r[2 * i]), b = cb * __uint_as_float(r[2 * i + 1]);
+    if (Epi == kTgPoly) {
+      const float2 f = TgPair<__half>::unpack(v[i]);
+      a += p.ca * f.x;
+      b += p.ca * f.y;
+    }
+    v[i] = TgPair<__half>::pack(a, b);
+  }
+  uint4* at = reinterpret_cast<uint4*>(out + (long long)m * p.ldo + row0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) at[i] = w[i];
+  if (k.m0 != k.n0) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < nrow)
+        reinterpret_cast<uint16_t*>(out)[(long long)(row0 + i) * p.ldo + m] =
+            (uint16_t)(i & 1 ? v[i >> 1] >> 16 : v[i >> 1]);
+  }
+}
+
+template <int Mode, int Epi, typename T>
+__device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t tmem, uint32_t rank, int warp, int first, int step) {
+  const int lane = ptx::lane_id();
+  const int quad = warp & 3, part = (warp - 4) >> 2;
+  const uint32_t leader_empty0 = ptx::mapa(ptx::smem_u32(&s.acc_empty[0]), 0);
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (int t = first; t < s.total; t += step) {
+    const TgTask k = tg_decode<Mode>(t, p, s);
+    const bool any = k.klen > 0;
+    if (any) {
+      bool ok = true;
+      if (lane == 0) ok = tg_wait(&s.acc_full[acc], acc_phase, p, s);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+      ptx::tc_fence_after();
+    }
+    const int m = k.m0 + (int)rank * 128 + quad * 32 + lane;
+    float2 bias = make_float2(0.f, 0.f);
+    float alpha = 1.f;
+    if (Epi == kTgStore) {
+      if (p.bias != nullptr && (m & ~1) < p.M)
+        bias = TgPair<T>::unpack(*reinterpret_cast<const uint32_t*>(reinterpret_cast<const T*>(p.bias) + (m & ~1)));
+    } else if (p.alpha != nullptr) {
+      alpha = p.alpha[k.g];
+    }
+    for (int c = part; c * 32 < k.nt; c += 2) {
+      uint32_t r[32];
+      __syncwarp();
+      if (any) {
+        ptx::tmem_ld32(tmem + acc * 256 + c * 32 + ((uint32_t)(quad * 32) << 16), r);
+        ptx::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = 0;
+      }
+      if (Epi == kTgGram || Epi == kTgPoly) tg_emit_symmetric<Epi>(r, p, k, k.n0 + c * 32, k.cols - c * 32, m, alpha);
+      else tg_emit_rows<Epi, T>(r, p, k, k.n0 + c * 32, k.cols - c * 32, m, lane, bias, alpha);
+    }
+    if (any) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+template <int Mode, bool PMn, bool QMn, int Epi, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
+    moe_tile_gemm_kernel(const __grid_constant__ TgParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TgSmem& s = *reinterpret_cast<TgSmem*>(tiles + (size_t)p.stages * p.stage_bytes);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      ptx::mbar_init(&s.full[i], 1);
+      ptx::mbar_init(&s.empty[i], 1);
+      ptx::mbar_init(&s.tail[i], 1);
+      ptx::mbar_init(&s.peer_tail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&s.acc_full[i], 1);
+      ptx::mbar_init(&s.acc_empty[i], 2 * kTgEpiWarps);
+    }
+    s.abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&p.tm_p);
+    for (int i = 0; i < (QMn ? 1 : 4); ++i) ptx::prefetch_tmap(&p.tm_q[i]);
+  }
+  if (warp == 3) {
+    ptx::tmem_alloc_pair(&s.tmem_base, kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  if (p.pdl) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+
+  const int mt = (p.M + 255) >> 8;
+  if (Mode == kTgRaggedN || Mode == kTgRaggedK) {
+    const int rows = Mode == kTgRaggedN ? p.N : p.K;
+    for (int e = threadIdx.x; e < p.groups; e += kTgThreads) {
+      int lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : rows;
+      if (lo < 0 || hi < lo || hi > rows) {
+        tg_set_error(p, s, kDevBounds, false);
+        lo = hi = 0;
+      }
+      s.start[e] = lo;
+      s.count[e] = hi - lo;
+    }
+  }
+  __syncthreads();
+  if (Mode == kTgRaggedN) {
+    if (warp == 0) {
+      int run = 0;
+      for (int b = 0; b < p.groups; b += 32) {
+        const int e = b + lane;
+        const int mine = e < p.groups ? (s.count[e] + p.nt - 1) / p.nt : 0;
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += up;
+        }
+        if (e < p.groups) s.tile0[e] = run + sum - mine;
+        run += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      if (lane == 0) {
+        s.tile0[p.groups] = run;
+        s.total = run * mt;
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    s.total = Mode == kTgSymmetric ? p.groups * (mt * (mt + 1) / 2) : p.groups * mt * ((p.N + p.nt - 1) / p.nt);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // both CTAs' barriers exist before any remote arrive
+  ptx::tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) tg_producer<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), rank, first, step);
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) tg_mma<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), tmem, first, step);
+  } else if (warp == 2) {
+    tg_tail_warp<Mode>(p, s, tiles, rank, first, step);
+  } else if (warp >= 4) {
+    tg_epilogue<Mode, Epi, T>(p, s, tmem, rank, warp, first, step);
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // no peer still arrives on this CTA's barriers or reads its tiles
+  ptx::tc_fence_after();
+  if (warp == 3) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+}  // namespace moe

@@ -1,0 +1,279 @@
+"""Operators around the MoE layer: products grouped by expert, the dense layer
+and its gradients, and the orthogonalised update of weight gradients.
+
+Argument checks and marshalling over the C entry points of the same names
+(include/moe_b200.h); every step runs in the library's CUDA kernels. Tensors
+are bf16 or fp16 on one CUDA device, the last index contiguous, rows a multiple
+of 8 elements apart. Work is enqueued on `stream` (default: the current stream
+of the tensors' device); nothing synchronises. `error_word`, an int32 tensor of
+one element, receives the call's device error code (0 = none).
+"""
+from __future__ import annotations
+
+import ctypes
+from contextlib import nullcontext
+from typing import Optional, Sequence, Union
+
+import torch
+
+from . import _ok, _ptr, _stream_handle, load_library
+
+DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+#: Newton-Schulz coefficients (a, b, c) of the quintic a t + b t^3 + c t^5 that drives singular values towards 1.
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def _tensor(t, name: str, dims: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name}: expected {dims} dimensions, got shape {tuple(t.shape)}")
+
+
+def _like(t, name: str, shape, dtype, device):
+    """Shape, type and device of a tensor; its last index must be contiguous."""
+    _tensor(t, name, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last index must be contiguous")
+
+
+def _whole(t, name: str, shape, dtype, device):
+    _like(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _pitch(t, name: str) -> int:
+    """Row pitch in elements of a [rows, width] tensor; a single row has its own width."""
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    ld = t.stride(0)
+    if ld < t.shape[1] or ld % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap (stride {ld})")
+    return ld
+
+
+def _half(t, name: str) -> int:
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name}: expected bfloat16 or float16, got {t.dtype}")
+    return DTYPE_CODES[t.dtype]
+
+
+def _cuda(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {sorted(k for k in ACTIVATIONS if k)} or None, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _error_word(t, device):
+    if t is not None:
+        _whole(t, "error_word", (1,), torch.int32, device)
+    return _ptr(t)
+
+
+def _on(device):
+    """The tensors' device as the current one for the call."""
+    return nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _workspace(nbytes: int, device, stream):
+    """Scratch of one call, taken from the allocator on the stream that uses it (so that it is
+    reused only by later work of that stream, and belongs to the graph when captured)."""
+    if not nbytes:
+        return None
+    with nullcontext() if stream is None else torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _offsets(offsets, device):
+    _tensor(offsets, "offsets", 1)
+    if offsets.shape[0] < 2:
+        raise ValueError("offsets: expected groups + 1 >= 2 values")
+    _whole(offsets, "offsets", offsets.shape, torch.int32, device)
+    return offsets.shape[0] - 1
+
+
+def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, transpose: bool = False,
+                   y: Optional[torch.Tensor] = None, error_word: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """y[r] = x[r] @ W[e] for offsets[e] <= r < offsets[e+1]; with ``transpose`` x[r] @ W[e].T.
+
+    x [rows, K], W [groups, K, N] contiguous ([groups, N, K] with ``transpose``), offsets int32
+    [groups + 1] on the device, not decreasing (``MoEPlan.routing``'s expert_offset fits; sizes
+    need no padding). Rows outside the groups are left as they were in a given y, undefined in a
+    new one. At most 1024 groups; K and N multiples of 8."""
+    _tensor(x, "x", 2)
+    _tensor(W, "W", 3)
+    dt = _half(x, "x")
+    rows, K = x.shape
+    groups = _offsets(offsets, x.device)
+    N = W.shape[1] if transpose else W.shape[2]
+    _like(x, "x", (rows, K), x.dtype, x.device)
+    _whole(W, "W", (groups, N, K) if transpose else (groups, K, N), x.dtype, x.device)
+    _cuda(x, "x")
+    if y is None:
+        y = torch.empty((rows, N), dtype=x.dtype, device=x.device)
+    _like(y, "y", (rows, N), x.dtype, x.device)
+    with _on(x.device):
+        _ok(load_library().moe_grouped_matmul(_ptr(x), _pitch(x, "x"), _ptr(W), _ptr(offsets), rows, groups, K, N,
+                                              1 if transpose else 0, dt, _ptr(y), _pitch(y, "y"),
+                                              _error_word(error_word, x.device), _stream_handle(stream, x.device)),
+            "moe_grouped_matmul")
+    return y
+
+
+def grouped_matmul_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor,
+                         dW: Optional[torch.Tensor] = None, error_word: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """dW[e] = x[rows of e].T @ dy[rows of e], [groups, K, N]; zeros for an empty group.
+    (``grouped_matmul(dy, W, offsets, transpose=True)`` is the input gradient.)"""
+    _tensor(x, "x", 2)
+    _tensor(dy, "dy", 2)
+    dt = _half(x, "x")
+    rows, K = x.shape
+    N = dy.shape[1]
+    groups = _offsets(offsets, x.device)
+    _like(x, "x", (rows, K), x.dtype, x.device)
+    _like(dy, "dy", (rows, N), x.dtype, x.device)
+    _cuda(x, "x")
+    if dW is None:
+        dW = torch.empty((groups, K, N), dtype=x.dtype, device=x.device)
+    _whole(dW, "dW", (groups, K, N), x.dtype, x.device)
+    with _on(x.device):
+        _ok(load_library().moe_grouped_matmul_wgrad(_ptr(x), _pitch(x, "x"), _ptr(dy), _pitch(dy, "dy"), _ptr(offsets),
+                                                    rows, groups, K, N, dt, _ptr(dW),
+                                                    _error_word(error_word, x.device),
+                                                    _stream_handle(stream, x.device)), "moe_grouped_matmul_wgrad")
+    return dW
+
+
+def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+           residual: Optional[torch.Tensor] = None, save_preact: bool = False, y: Optional[torch.Tensor] = None,
+           preact: Optional[torch.Tensor] = None, error_word: Optional[torch.Tensor] = None, stream=None):
+    """act(x @ W + bias) + residual in one kernel: x [T, K], W [K, N], bias [N], residual [T, N].
+
+    activation: None, "relu", "gelu" (erf), "gelu_tanh" or "silu". With ``save_preact`` (or a
+    given ``preact``) returns (y, z), z = x @ W + bias as linear_backward takes it. y may be the
+    residual itself."""
+    _tensor(x, "x", 2)
+    _tensor(W, "W", 2)
+    dt, act = _half(x, "x"), _activation(activation)
+    T, K = x.shape
+    N = W.shape[1]
+    dev = x.device
+    _like(x, "x", (T, K), x.dtype, dev)
+    _whole(W, "W", (K, N), x.dtype, dev)
+    if bias is not None:
+        _whole(bias, "bias", (N,), x.dtype, dev)
+    if residual is not None:
+        _like(residual, "residual", (T, N), x.dtype, dev)
+    _cuda(x, "x")
+    if y is None:
+        y = torch.empty((T, N), dtype=x.dtype, device=dev)
+    _like(y, "y", (T, N), x.dtype, dev)
+    if preact is None and save_preact:
+        preact = torch.empty((T, N), dtype=x.dtype, device=dev)
+    if preact is not None:
+        _like(preact, "preact", (T, N), x.dtype, dev)
+    with _on(dev):
+        _ok(load_library().moe_linear(_ptr(x), _pitch(x, "x"), _ptr(W), _ptr(bias), _ptr(residual),
+                                      0 if residual is None else _pitch(residual, "residual"), T, K, N, act, dt,
+                                      _ptr(y), _pitch(y, "y"), _ptr(preact),
+                                      0 if preact is None else _pitch(preact, "preact"),
+                                      _error_word(error_word, dev), _stream_handle(stream, dev)), "moe_linear")
+    return y if preact is None else (y, preact)
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, preact: Optional[torch.Tensor] = None,
+                    activation: Optional[str] = None, input_grad: bool = True, weight_grad: bool = True,
+                    bias_grad: bool = False, error_word: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ``linear`` for the upstream dy [T, N]: dict of dx [T, K], dW [K, N] and
+    dbias [N] (None where not asked for). preact: the z that linear returned, needed with an
+    activation. The residual's gradient is dy itself."""
+    _tensor(dy, "dy", 2)
+    _tensor(x, "x", 2)
+    _tensor(W, "W", 2)
+    dt, act = _half(x, "x"), _activation(activation)
+    T, K = x.shape
+    N = W.shape[1]
+    dev = x.device
+    _like(x, "x", (T, K), x.dtype, dev)
+    _whole(W, "W", (K, N), x.dtype, dev)
+    _like(dy, "dy", (T, N), x.dtype, dev)
+    if act and preact is None:
+        raise ValueError("preact is needed with an activation")
+    z = preact if act else None
+    if z is not None:
+        _like(z, "preact", (T, N), x.dtype, dev)
+    _cuda(x, "x")
+    lib = load_library()
+    with _on(dev):
+        dx = torch.empty((T, K), dtype=x.dtype, device=dev) if input_grad else None
+        dW = torch.empty((K, N), dtype=x.dtype, device=dev) if weight_grad else None
+        dbias = torch.empty((N,), dtype=x.dtype, device=dev) if bias_grad else None
+        nbytes = lib.moe_linear_backward_workspace_bytes(T, N, act, 1 if bias_grad else 0)
+        ws = _workspace(nbytes, dev, stream)
+        _ok(lib.moe_linear_backward(_ptr(dy), _pitch(dy, "dy"), _ptr(x), _pitch(x, "x"), _ptr(W), _ptr(z),
+                                    0 if z is None else _pitch(z, "preact"), T, K, N, act, dt, _ptr(dx), K, _ptr(dW),
+                                    _ptr(dbias), _ptr(ws), nbytes, _error_word(error_word, dev),
+                                    _stream_handle(stream, dev)), "moe_linear_backward")
+    return dict(dx=dx, dW=dW, dbias=dbias)
+
+
+def orthogonalize(G: torch.Tensor, steps: int = 5,
+                  coeffs: Union[Sequence[float], Sequence[Sequence[float]]] = QUINTIC, eps: float = 1e-7,
+                  out: Optional[torch.Tensor] = None, error_word: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of G [m, n] or of every matrix of G [batch, m, n]
+    (weight gradients: ``MoEPlan.backward``'s dW1, dW3, dW2, ``grouped_matmul_wgrad``'s or
+    ``linear_backward``'s dW). X = G / (|G|_F + eps), then ``steps`` times
+    X <- a X + (b A + c A A) X with A = X X^T (the short side inside). G bf16 or fp32 of any size
+    and row pitch; returns bf16 of G's shape. coeffs: one (a, b, c) for all steps, or one per step."""
+    if not isinstance(G, torch.Tensor):
+        raise TypeError("G must be a torch.Tensor")
+    if G.dim() not in (2, 3) or G.shape[-1] < 1 or G.shape[-2] < 1:
+        raise ValueError(f"G: expected [m, n] or [batch, m, n], got {tuple(G.shape)}")
+    if G.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"G: expected bfloat16 or float32, got {G.dtype}")
+    if steps < 1:
+        raise ValueError("steps must be at least 1")
+    rows = [list(c) for c in coeffs] if isinstance(coeffs[0], (list, tuple)) else [list(coeffs)] * steps
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coeffs: expected (a, b, c), or one such triple for each step")
+    _like(G, "G", G.shape, G.dtype, G.device)
+    _cuda(G, "G")
+    dev = G.device
+    if out is None:
+        out = torch.empty(G.shape, dtype=torch.bfloat16, device=dev)
+    _like(out, "out", G.shape, torch.bfloat16, dev)
+
+    def pitches(t, name):
+        t = t if t.dim() == 3 else t.unsqueeze(0)
+        ld = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+        bs = t.stride(0) if t.shape[0] > 1 else ld * t.shape[1]
+        if ld < t.shape[2] or (t.shape[0] > 1 and bs < ld * (t.shape[1] - 1) + t.shape[2]):
+            raise ValueError(f"{name}: rows or matrices overlap")
+        return ld, bs
+
+    batch, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
+    lib = load_library()
+    flat = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+    with _on(dev):
+        nbytes = lib.moe_orthogonalize_workspace_bytes(batch, m, n)
+        ws = _workspace(nbytes, dev, stream)
+        _ok(lib.moe_orthogonalize(_ptr(G), *pitches(G, "G"), batch, m, n, DTYPE_CODES[G.dtype], steps, flat, eps,
+                                  _ptr(out), *pitches(out, "out"), _ptr(ws), nbytes, _error_word(error_word, dev),
+                                  _stream_handle(stream, dev)), "moe_orthogonalize")
+    return out
