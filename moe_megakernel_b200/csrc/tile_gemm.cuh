@@ -37,7 +37,7 @@ constexpr int kTgMaxStages = 12;
 constexpr int kTgMaxGroups = 1024;
 constexpr int kTgABytes = 128 * 128;     // 128 rows of P, 64 k each
 constexpr int kTgSmemTiles = 200 * 1024; // stages fill at most this
-constexpr unsigned long long kTgTimeoutNs = 2000000000ull;
+constexpr long long kTgTimeoutCycles = 4000000000ll;   // about two seconds
 
 enum TgMode : int {
   kTgRaggedN = 0,    // groups of N-side rows, one P per group (offsets == null: one group of all rows)
@@ -118,18 +118,31 @@ __device__ __forceinline__ void tg_set_error(const TgParams& p, TgSmem& s, int c
   if (stop) *reinterpret_cast<volatile int*>(&s.abort) = 1;
 }
 
-// Bounded wait of one thread on a local barrier phase.
+// Bounded wait on a local barrier phase, by one thread or by a whole warp (all
+// lanes poll; tg_wait_warp's answer is the same in every lane). The bound is on
+// SM cycles, which are cheap to read.
 __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, const TgParams& p, TgSmem& s) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
+  const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
-    if (ptx::globaltimer() - t0 > kTgTimeoutNs) {
+    if (clock64() - t0 > kTgTimeoutCycles) {
       tg_set_error(p, s, kDevTimeout, true);
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ bool tg_wait_warp(uint64_t* bar, uint32_t parity, const TgParams& p, TgSmem& s) {
+  const bool ok = tg_wait(bar, parity, p, s);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool tg_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // Position of tile `idx` in a grid of mt x ntl tiles: bands of 8 M tiles, all
@@ -265,20 +278,21 @@ __device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32
     const int pbatch = Mode == kTgRaggedK ? 0 : k.g;
     const int qbatch = Mode == kTgRaggedK || Mode == kTgRaggedN ? 0 : k.g;
     for (int kb = 0; kb < nk; ++kb) {
-      if (!tg_wait(&s.empty[stage], phase ^ 1, p, s)) {
+      if (!tg_wait_warp(&s.empty[stage], phase ^ 1, p, s)) {
         ok = false;
         break;
       }
       const uint32_t dst = tiles + stage * p.stage_bytes;
-      uint32_t bar;
-      if (tg_has_tail<Mode>(k, kb)) {
-        ptx::mbar_arrive_expect_tx(&s.tail[stage], tx);
-        bar = ptx::mapa(ptx::smem_u32(&s.tail[stage]), rank);
-      } else {
-        if (rank == 0) ptx::mbar_arrive_expect_tx(&s.full[stage], 2 * tx);
-        bar = ptx::mapa(ptx::smem_u32(&s.full[stage]), 0);
+      const bool tail = tg_has_tail<Mode>(k, kb);
+      // both CTAs' bytes on the leader's barrier; a tail block's on each CTA's own
+      const uint32_t bar = tail ? ptx::mapa(ptx::smem_u32(&s.tail[stage]), rank)
+                                : ptx::mapa(ptx::smem_u32(&s.full[stage]), 0);
+      if (tg_elect()) {
+        if (tail) ptx::mbar_arrive_expect_tx(&s.tail[stage], tx);
+        else if (rank == 0) ptx::mbar_arrive_expect_tx(&s.full[stage], 2 * tx);
+        tg_load_stage<PMn, QMn>(dst, p, k, k.k0 + kb * 64, rank, bar, pbatch, qbatch);
       }
-      tg_load_stage<PMn, QMn>(dst, p, k, k.k0 + kb * 64, rank, bar, pbatch, qbatch);
+      __syncwarp();
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
@@ -287,15 +301,14 @@ __device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32
   }
   // the commits that free the stages have arrived before this CTA's barriers go away
   for (int i = 0; ok && i < p.stages; ++i) {
-    ok = tg_wait(&s.empty[stage], phase ^ 1, p, s);
+    ok = tg_wait_warp(&s.empty[stage], phase ^ 1, p, s);
     if (++stage == p.stages) {
       stage = 0;
       phase ^= 1;
     }
   }
   if (!ok) {   // given up: let the copies in flight land before the shared memory goes away
-    const uint64_t t0 = ptx::globaltimer();
-    while (ptx::globaltimer() - t0 < 5000000ull) __nanosleep(1000);
+    for (int i = 0; i < 5000; ++i) __nanosleep(1000);
   }
 }
 
@@ -316,9 +329,7 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint3
     if (nk == 0) continue;
     const int last = (stage + nk - 1) % p.stages;
     if (tg_has_tail<Mode>(k, nk - 1)) {
-      bool ok = true;
-      if (lane == 0) ok = tg_wait(&s.tail[last], (used >> last) & 1, p, s);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+      if (!tg_wait_warp(&s.tail[last], (used >> last) & 1, p, s)) return;
       const int r0 = k.klen & 63, r1 = (r0 + 15) & ~15;
       const int boxes = 2 + (((k.nt >> 1) + 63) >> 6);
       uint8_t* at = tiles + (size_t)last * p.stage_bytes;
@@ -327,21 +338,11 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint3
           *reinterpret_cast<uint4*>(at + b * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
       ptx::fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) {
-        if (rank != 0) {
-          ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&s.peer_tail[last]), 0));
-        } else {
-          uint64_t* bar = &s.peer_tail[last];
-          const uint64_t t0 = ptx::globaltimer();
-          while (!ptx::mbar_try_wait_cluster(bar, (used >> last) & 1)) {
-            if (*reinterpret_cast<volatile int*>(&s.abort)) break;
-            if (ptx::globaltimer() - t0 > kTgTimeoutNs) {
-              tg_set_error(p, s, kDevTimeout, true);
-              break;
-            }
-          }
-          ptx::mbar_arrive(&s.full[last]);
-        }
+      if (rank != 0) {
+        if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&s.peer_tail[last]), 0));
+      } else {   // in place of the producer's arrival, once both CTAs' blocks are clean
+        if (!tg_wait_warp(&s.peer_tail[last], (used >> last) & 1, p, s)) return;
+        if (lane == 0) ptx::mbar_arrive(&s.full[last]);
       }
       __syncwarp();
       used ^= 1u << last;
@@ -351,11 +352,19 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint3
 }
 
 // ---------------------------------------------------------------- MMA (leader)
+// The warp runs the loop together and one lane issues: the descriptors are then
+// warp-uniform values. With the loop inside a one-lane branch an MMA took 70
+// cycles to issue, more than its share of the tensor core's time (64 at 256
+// columns and two CTAs' operands).
 template <int Mode, bool PMn, bool QMn>
 __device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tmem, int first, int step) {
   const uint32_t fmt = p.f16 ? 0u : 1u;
   const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((PMn ? 1u : 0u) << 15) | ((QMn ? 1u : 0u) << 16) |
                           ((256u >> 4) << 24);
+  const uint64_t pdesc = PMn ? ptx::smem_desc_sw128(tiles, 8192, 1024) : ptx::smem_desc_sw128(tiles, 16, 1024);
+  const uint64_t qdesc = QMn ? ptx::smem_desc_sw128(tiles + kTgABytes, 8192, 1024)
+                             : ptx::smem_desc_sw128(tiles + kTgABytes, 16, 1024);
+  constexpr uint64_t pstep = (PMn ? 2048 : 32) >> 4, qstep = (QMn ? 2048 : 32) >> 4;   // 16 k further
   int stage = 0;
   uint32_t phase = 0;
   int acc = 0;
@@ -364,32 +373,29 @@ __device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tm
     const TgTask k = tg_decode<Mode>(t, p, s);
     const int nk = (k.klen + 63) >> 6;
     if (nk == 0) continue;
-    if (!tg_wait(&s.acc_empty[acc], acc_phase ^ 1, p, s)) return;
+    if (!tg_wait_warp(&s.acc_empty[acc], acc_phase ^ 1, p, s)) return;
     ptx::tc_fence_after();
     const uint32_t d = tmem + acc * 256;
     const uint32_t idesc = idesc0 | ((uint32_t)(k.nt >> 3) << 17);
     for (int kb = 0; kb < nk; ++kb) {
-      if (!tg_wait(&s.full[stage], phase, p, s)) return;
+      if (!tg_wait_warp(&s.full[stage], phase, p, s)) return;
       ptx::tc_fence_after();
-      const uint32_t a = tiles + stage * p.stage_bytes;
-      const uint32_t b = a + kTgABytes;
+      const uint64_t off = (uint64_t)(uint32_t)(stage * p.stage_bytes) >> 4;
       const int steps = Mode == kTgRaggedK ? tg_ksteps(k, kb) : 4;
+      if (tg_elect()) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (Mode == kTgRaggedK && kk >= steps) break;
-        const uint64_t ad = PMn ? ptx::smem_desc_sw128(a + kk * 2048, 8192, 1024)
-                                : ptx::smem_desc_sw128(a + kk * 32, 16, 1024);
-        const uint64_t bd = QMn ? ptx::smem_desc_sw128(b + kk * 2048, 8192, 1024)
-                                : ptx::smem_desc_sw128(b + kk * 32, 16, 1024);
-        ptx::mma_bf16_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          if (Mode != kTgRaggedK || kk < steps)
+            ptx::mma_bf16_pair(d, pdesc + off + kk * pstep, qdesc + off + kk * qstep, idesc, (kb | kk) != 0 ? 1u : 0u);
+        ptx::mma_commit_pair_multicast(&s.empty[stage], 0x3);
+        if (kb == nk - 1) ptx::mma_commit_pair_multicast(&s.acc_full[acc], 0x3);
       }
-      ptx::mma_commit_pair_multicast(&s.empty[stage], 0x3);
+      __syncwarp();
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
       }
     }
-    ptx::mma_commit_pair_multicast(&s.acc_full[acc], 0x3);
     if (++acc == 2) {
       acc = 0;
       acc_phase ^= 1;
@@ -421,14 +427,27 @@ struct TgPair<__half> {
   }
 };
 
-__device__ __forceinline__ float tg_act(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f || z != z ? z : 0.f;
-    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case kActGeluTanh: return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    case kActSilu: return z / (1.f + expf(-z));
-    default: return z;
-  }
+template <int Act>
+__device__ __forceinline__ float tg_act(float z) {
+  if (Act == kActRelu) return z > 0.f || z != z ? z : 0.f;
+  if (Act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (Act == kActGeluTanh) return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+  if (Act == kActSilu) return z / (1.f + expf(-z));
+  return z;
+}
+template <int Act>
+__device__ __forceinline__ void tg_act_all(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(tg_act<Act>(__uint_as_float(r[i])));
+}
+// One branch per 32 values: chosen inside the loop, the five functions' code
+// (each inlined per value) was jumped over for every value.
+__device__ __forceinline__ void tg_act32(uint32_t (&r)[32], int act) {
+  if (act == kActNone) return;
+  if (act == kActRelu) tg_act_all<kActRelu>(r);
+  else if (act == kActGelu) tg_act_all<kActGelu>(r);
+  else if (act == kActGeluTanh) tg_act_all<kActGeluTanh>(r);
+  else tg_act_all<kActSilu>(r);
 }
 
 // 32 accumulator columns of one warp: lane l holds column m (= m0 + l) of 32
@@ -458,24 +477,31 @@ __device__ __forceinline__ void tg_emit_rows(uint32_t (&r)[32], const TgParams& 
       for (int i = 0; i < 16; ++i)
         v[i] = 2 * i + odd < nrow ? *reinterpret_cast<const uint32_t*>(res + 2 * i * p.ldr) : 0u;
     }
-    T* out = reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)(row0 + odd) * p.ldo + m2;
-    T* z = reinterpret_cast<T*>(p.z) + (long long)(row0 + odd) * p.ldz + m2;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (2 * i + odd >= nrow) break;
-      float a = __uint_as_float(r[2 * i]) + bias.x, b = __uint_as_float(r[2 * i + 1]) + bias.y;
-      if (p.z != nullptr) *reinterpret_cast<uint32_t*>(z + 2 * i * p.ldz) = TgPair<T>::pack(a, b);
-      if (p.act != kActNone) {
-        a = tg_act(a, p.act);
-        b = tg_act(b, p.act);
-      }
-      if (p.res != nullptr) {
-        const float2 f = TgPair<T>::unpack(v[i]);
-        a += f.x;
-        b += f.y;
-      }
-      *reinterpret_cast<uint32_t*>(out + 2 * i * p.ldo) = TgPair<T>::pack(a, b);
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + (i & 1 ? bias.y : bias.x));
+    if (p.z != nullptr) {
+      T* z = reinterpret_cast<T*>(p.z) + (long long)(row0 + odd) * p.ldz + m2;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (2 * i + odd < nrow)
+          *reinterpret_cast<uint32_t*>(z + 2 * i * p.ldz) =
+              TgPair<T>::pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
     }
+    tg_act32(r, p.act);
+    if (p.res != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = TgPair<T>::unpack(v[i]);
+        r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) + f.x);
+        r[2 * i + 1] = __float_as_uint(__uint_as_float(r[2 * i + 1]) + f.y);
+      }
+    }
+    T* out = reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)(row0 + odd) * p.ldo + m2;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i + odd < nrow)
+        *reinterpret_cast<uint32_t*>(out + 2 * i * p.ldo) =
+            TgPair<T>::pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
   } else {
     // the pair (m2, m2 + 1) lies in the padded pitch even where m2 + 1 is past the matrix
     const long long at = k.g * p.in_bs + (long long)(row0 + odd) * p.ldi + m2;
@@ -681,9 +707,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 0) {
-    if (lane == 0) tg_producer<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), rank, first, step);
+    tg_producer<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), rank, first, step);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) tg_mma<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), tmem, first, step);
+    if (rank == 0) tg_mma<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), tmem, first, step);
   } else if (warp == 2) {
     tg_tail_warp<Mode>(p, s, tiles, rank, first, step);
   } else if (warp >= 4) {
