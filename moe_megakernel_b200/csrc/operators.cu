@@ -81,11 +81,13 @@ int current_device(int* num_sms) {
   return d;
 }
 
-// Stages that fit for the largest N tile (`nt`) of a launch.
+// Stages that fit beside the epilogue's pieces for the largest N tile (`nt`) of a launch.
+template <int Epi>
 void size_stages(TgParams& p, bool q_mn) {
   const int half = p.nt / 2;
   p.stage_bytes = kTgABytes + (q_mn ? (half + 63) / 64 * 8192 : half * 128);
-  p.stages = std::min(kTgMaxStages, kTgSmemTiles / p.stage_bytes);
+  p.epi_bytes = tg_epi_bytes<Epi>(p.res != nullptr);
+  p.stages = std::min(kTgMaxStages, (kTgSmemMax - (int)tg_smem_bytes(0, 0, p.epi_bytes)) / p.stage_bytes);
 }
 
 // One launch. `tiles`: output tiles where the host knows them, else 0 (the
@@ -105,18 +107,17 @@ int launch(TgParams& p, long long tiles, bool pdl, cudaStream_t st) {
   cfg.attrs = at;
   int c = clusters[d].load();
   if (c == 0) {
-    const int most = (int)tg_smem_bytes(1, kTgSmemTiles);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTgSmemMax) != cudaSuccess)
       return MOE_ERR_CUDA;
     cfg.gridDim = dim3(2 * (sms / 2));
-    cfg.dynamicSmemBytes = most;
+    cfg.dynamicSmemBytes = kTgSmemMax;
     if (cudaOccupancyMaxActiveClusters(&c, kernel, &cfg) != cudaSuccess || c < 1) return MOE_ERR_CUDA;
     clusters[d].store(c);
   }
-  size_stages(p, QMn);
+  size_stages<Epi>(p, QMn);
   p.pdl = pdl ? 1 : 0;
   cfg.gridDim = dim3(2 * (unsigned)(tiles > 0 && tiles < c ? tiles : c));
-  cfg.dynamicSmemBytes = tg_smem_bytes(p.stages, p.stage_bytes);
+  cfg.dynamicSmemBytes = tg_smem_bytes(p.stages, p.stage_bytes, p.epi_bytes);
   if (pdl) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

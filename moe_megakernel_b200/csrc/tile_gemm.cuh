@@ -36,7 +36,6 @@ constexpr int kTgEpiWarps = 8;
 constexpr int kTgMaxStages = 12;
 constexpr int kTgMaxGroups = 1024;
 constexpr int kTgABytes = 128 * 128;     // 128 rows of P, 64 k each
-constexpr int kTgSmemTiles = 200 * 1024; // stages fill at most this
 constexpr long long kTgTimeoutCycles = 4000000000ll;   // about two seconds
 
 enum TgMode : int {
@@ -62,7 +61,7 @@ struct TgParams {
   int M, N, K;           // extents (N: rows of Q in a ragged-N product; K: rows in a ragged-K one)
   int groups;            // groups or batches
   int nt;                // largest N tile: 32, 64, 128 or 256
-  int stages, stage_bytes;
+  int stages, stage_bytes, epi_bytes;
   int f16;               // operands are fp16 (else bf16)
   const int32_t* offsets;   // [groups + 1] device, or null
   int32_t* err;             // device error word, or null
@@ -100,8 +99,9 @@ struct TgSmem {
   int tile0[kTgMaxGroups + 1];   // first N tile of each group (ragged N)
 };
 
-constexpr size_t tg_smem_bytes(int stages, int stage_bytes) {
-  return 1024 + (size_t)stages * stage_bytes + sizeof(TgSmem);
+constexpr int kTgSmemMax = 232448;   // shared memory of a CTA
+constexpr size_t tg_smem_bytes(int stages, int stage_bytes, int epi_bytes) {
+  return 1024 + (size_t)stages * stage_bytes + epi_bytes + sizeof(TgSmem);
 }
 
 struct TgTask {
@@ -436,183 +436,342 @@ __device__ __forceinline__ float tg_act(float z) {
   return z;
 }
 template <int Act>
-__device__ __forceinline__ void tg_act_all(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tg_act_each(uint32_t (&r)[2][16]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(tg_act<Act>(__uint_as_float(r[i])));
+  for (int i = 0; i < 32; ++i) r[i >> 4][i & 15] = __float_as_uint(tg_act<Act>(__uint_as_float(r[i >> 4][i & 15])));
 }
 // One branch per 32 values: chosen inside the loop, the five functions' code
 // (each inlined per value) was jumped over for every value.
-__device__ __forceinline__ void tg_act32(uint32_t (&r)[32], int act) {
+__device__ __forceinline__ void tg_act_all(uint32_t (&r)[2][16], int act) {
   if (act == kActNone) return;
-  if (act == kActRelu) tg_act_all<kActRelu>(r);
-  else if (act == kActGelu) tg_act_all<kActGelu>(r);
-  else if (act == kActGeluTanh) tg_act_all<kActGeluTanh>(r);
-  else tg_act_all<kActSilu>(r);
+  if (act == kActRelu) tg_act_each<kActRelu>(r);
+  else if (act == kActGelu) tg_act_each<kActGelu>(r);
+  else if (act == kActGeluTanh) tg_act_each<kActGeluTanh>(r);
+  else tg_act_each<kActSilu>(r);
 }
 
-// 32 accumulator columns of one warp: lane l holds column m (= m0 + l) of 32
-// consecutive output rows, row0 .. row0 + 31, of which nrow exist.
+// A warp works on 32 x 32 pieces of the accumulator: 32 M rows (its TMEM lanes)
+// by 32 N columns. tcgen05.ld.16x256b hands each thread, for every 8 x 8 block,
+// two neighbouring n of one m - the fragment that stmatrix and ldmatrix move to
+// and from shared memory, transposed on request. So the piece is turned to
+// output order (n rows of contiguous m) by four stmatrix, copied out as 16-byte
+// vectors (8 rows of 64 bytes per instruction), and what the epilogue reads (the
+// residual, X, A) comes in the same way, copied ahead with cp.async. Storing
+// straight from a 32x32b load took about 490 instructions a piece, mostly lane
+// swaps and addresses, and held the weight gradient at 1.6 TB/s.
 //
-// Row-wise outputs: neighbouring lanes swap halves so that each holds two
-// consecutive columns of one row; a store instruction then covers two rows of
-// 64 contiguous bytes with 4 bytes per lane. What the epilogue reads (the
-// residual, X) is loaded for all 32 rows before the first use.
-template <int Epi, typename T>
-__device__ __forceinline__ void tg_emit_rows(uint32_t (&r)[32], const TgParams& p, const TgTask& k, int row0, int nrow,
-                                             int m, int lane, float2 bias, float alpha) {
-  const int odd = lane & 1;
-  const int m2 = m - odd;
-  if (m2 >= p.M) nrow = 0;   // still takes part in the swaps
+// A piece in shared memory: 32 rows of 64 bytes, the row's 16-byte chunk c at
+// place c ^ (row / 2 % 4), which spreads both the matrix and the row accesses
+// over all banks.
+constexpr int kTgPiece = 2048;
+__device__ __forceinline__ uint32_t tg_piece_at(int row, int c) { return row * 64 + ((c ^ ((row >> 1) & 3)) << 4); }
+
+__device__ __forceinline__ void tg_tmem_frag(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Four 8 x 8 matrices whose rows start at the addresses of lanes 0-7, 8-15, 16-23, 24-31.
+template <bool Trans>
+__device__ __forceinline__ void tg_stmatrix(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  if (Trans)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+  else
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+template <bool Trans>
+__device__ __forceinline__ void tg_ldmatrix(uint32_t at, uint32_t (&v)[4]) {
+  if (Trans)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 tg_lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// One piece as a thread holds it: v[4 i + b] packs n = 8 i + 2 (lane % 4) and
+// n + 1 of m = 8 b + lane / 4.
+// To shared memory as n rows of m (kRows = N) or as m rows of n (kRows = M).
+enum TgRows { kRowsN, kRowsM };
+template <TgRows R>
+__device__ __forceinline__ void tg_piece_put(uint32_t piece, const uint32_t (&v)[16], int lane) {
+  const int j = lane >> 3, r = lane & 7;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[2 * i] : r[2 * i + 1], 1);
-    if (odd) r[2 * i] = got;
-    else r[2 * i + 1] = got;
+  for (int i = 0; i < 4; ++i) {
+    if (R == kRowsN) tg_stmatrix<true>(piece + tg_piece_at(8 * i + r, j), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    else tg_stmatrix<false>(piece + tg_piece_at(8 * i + r, j), v[i], v[4 + i], v[8 + i], v[12 + i]);
   }
+}
+template <TgRows R>
+__device__ __forceinline__ void tg_piece_get(uint32_t piece, uint32_t (&v)[16], int lane) {
+  const int j = lane >> 3, r = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+    if (R == kRowsN) {
+      tg_ldmatrix<true>(piece + tg_piece_at(8 * i + r, j), w);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v[4 * i + b] = w[b];
+    } else {
+      tg_ldmatrix<false>(piece + tg_piece_at(8 * i + r, j), w);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v[4 * b + i] = w[b];
+    }
+  }
+}
+
+// Copies a piece to / from `rows` global rows (2-byte elements, pitch ld, every
+// row 16-byte aligned) of which the first `cols` columns (a multiple of 8) exist.
+__device__ __forceinline__ void tg_piece_out(uint32_t piece, void* g, long long ld, int rows, int cols, int lane) {
+  const int c = lane & 3;
+  uint16_t* at = reinterpret_cast<uint16_t*>(g) + (lane >> 2) * ld + c * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2);
+    if (row < rows && c * 8 < cols) *reinterpret_cast<uint4*>(at + i * 8 * ld) = tg_lds16(piece + tg_piece_at(row, c));
+  }
+}
+__device__ __forceinline__ void tg_piece_in(uint32_t piece, const void* g, long long ld, int rows, int cols, int lane) {
+  const int c = lane & 3;
+  const uint16_t* at = reinterpret_cast<const uint16_t*>(g) + (lane >> 2) * ld + c * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2);
+    if (row < rows && c * 8 < cols) ptx::cp_async_16(piece + tg_piece_at(row, c), at + i * 8 * ld);
+  }
+}
+// The same for rows of any alignment and length.
+__device__ __forceinline__ void tg_piece_out_any(uint32_t piece, uint16_t* g, long long ld, int rows, int cols, int lane) {
+  if (lane >= cols) return;
+  for (int row = 0; row < rows; ++row) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(piece + tg_piece_at(row, lane >> 3) + (lane & 7) * 2) : "memory");
+    g[row * ld + lane] = v;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void tg_pack(const uint32_t (&r)[2][16], uint32_t (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      v[4 * i + b] = TgPair<T>::pack(__uint_as_float(r[b >> 1][4 * i + 2 * (b & 1)]),
+                                     __uint_as_float(r[b >> 1][4 * i + 2 * (b & 1) + 1]));
+}
+
+// Pieces a warp keeps in shared memory: two slots when the epilogue reads (the
+// next piece's input is on its way while this one is worked on), each of one
+// plane, or two where X comes as a pair.
+template <int Epi>
+__host__ __device__ constexpr int tg_planes() { return Epi == kTgUpdate || Epi == kTgUpdateOut ? 2 : 1; }
+template <int Epi>
+__host__ __device__ constexpr int tg_epi_bytes(bool residual) {
+  return kTgEpiWarps * tg_planes<Epi>() * kTgPiece * (Epi == kTgStore && !residual ? 1 : 2);
+}
+
+template <int Epi, typename T>
+__device__ __forceinline__ void tg_prefetch(uint32_t slot, const TgParams& p, const TgTask& k, int c, int m, int lane) {
+  const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
+  if (mcol > 0) {
+    if (Epi == kTgStore) {
+      tg_piece_in(slot, reinterpret_cast<const T*>(p.res) + (long long)row0 * p.ldr + m, p.ldr, nrow, mcol, lane);
+    } else if (Epi == kTgPoly) {   // rows of A (m), whose pitch reaches past the last column
+      tg_piece_in(slot, p.in + k.g * p.in_bs + (long long)m * p.ldi + row0, p.ldi, mcol, 32, lane);
+    } else if (Epi == kTgUpdate || Epi == kTgUpdateOut) {
+      const long long at = k.g * p.in_bs + (long long)row0 * p.ldi + m;
+      tg_piece_in(slot, p.in + at, p.ldi, nrow, 32, lane);
+      tg_piece_in(slot + kTgPiece, p.lo + at, p.ldi, nrow, 32, lane);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// One piece: r holds its accumulator, `slot` its shared memory (inputs landed).
+// m is the piece's first column of the output, bias[b] belongs to m + 8 b + lane / 4.
+template <int Epi, typename T>
+__device__ __forceinline__ void tg_piece(uint32_t slot, uint32_t (&r)[2][16], const TgParams& p, const TgTask& k, int c,
+                                         int m, int lane, const float (&bias)[4], float alpha) {
+  const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
+  uint32_t v[16];
   if (Epi == kTgStore) {
-    uint32_t v[16];
-    if (p.res != nullptr) {
-      const T* res = reinterpret_cast<const T*>(p.res) + (long long)(row0 + odd) * p.ldr + m2;
+    uint32_t res[16];
+    if (p.res != nullptr) tg_piece_get<kRowsN>(slot, res, lane);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[i] = 2 * i + odd < nrow ? *reinterpret_cast<const uint32_t*>(res + 2 * i * p.ldr) : 0u;
-    }
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + (i & 1 ? bias.y : bias.x));
-    if (p.z != nullptr) {
-      T* z = reinterpret_cast<T*>(p.z) + (long long)(row0 + odd) * p.ldz + m2;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (2 * i + odd < nrow)
-          *reinterpret_cast<uint32_t*>(z + 2 * i * p.ldz) =
-              TgPair<T>::pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-    }
-    tg_act32(r, p.act);
-    if (p.res != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 f = TgPair<T>::unpack(v[i]);
-        r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) + f.x);
-        r[2 * i + 1] = __float_as_uint(__uint_as_float(r[2 * i + 1]) + f.y);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
+        e[0] = __float_as_uint(__uint_as_float(e[0]) + bias[b]);
+        e[1] = __float_as_uint(__uint_as_float(e[1]) + bias[b]);
       }
+    if (p.z != nullptr) {
+      tg_pack<T>(r, v);
+      __syncwarp();
+      tg_piece_put<kRowsN>(slot, v, lane);
+      __syncwarp();
+      tg_piece_out(slot, reinterpret_cast<T*>(p.z) + (long long)row0 * p.ldz + m, p.ldz, nrow, mcol, lane);
     }
-    T* out = reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)(row0 + odd) * p.ldo + m2;
+    tg_act_all(r, p.act);
+    if (p.res != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (2 * i + odd < nrow)
-        *reinterpret_cast<uint32_t*>(out + 2 * i * p.ldo) =
-            TgPair<T>::pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float2 f = TgPair<T>::unpack(res[4 * i + b]);
+          uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
+          e[0] = __float_as_uint(__uint_as_float(e[0]) + f.x);
+          e[1] = __float_as_uint(__uint_as_float(e[1]) + f.y);
+        }
+    }
+    tg_pack<T>(r, v);
+    __syncwarp();
+    tg_piece_put<kRowsN>(slot, v, lane);
+    __syncwarp();
+    tg_piece_out(slot, reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol,
+                 lane);
+  } else if (Epi == kTgGram || Epi == kTgPoly) {
+    // A = X X^T and B = b A + c A A are symmetric: the piece goes out as it lies (row m, whose pitch
+    // is padded to 64, so whole pieces fit) and, off the diagonal tiles, transposed to the mirrored place
+    const float cb = p.cb * alpha * alpha;
+    if (Epi == kTgPoly) tg_piece_get<kRowsM>(slot, v, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
+        float x = cb * __uint_as_float(e[0]), y = cb * __uint_as_float(e[1]);
+        if (Epi == kTgPoly) {
+          const float2 f = TgPair<__half>::unpack(v[4 * i + b]);
+          x += p.ca * f.x;
+          y += p.ca * f.y;
+        }
+        v[4 * i + b] = TgPair<__half>::pack(x, y);
+      }
+    __half* out = reinterpret_cast<__half*>(p.out) + k.g * p.out_bs;
+    __syncwarp();
+    tg_piece_put<kRowsM>(slot, v, lane);
+    __syncwarp();
+    tg_piece_out(slot, out + (long long)m * p.ldo + row0, p.ldo, mcol, 32, lane);
+    if (k.m0 != k.n0) {
+      __syncwarp();
+      tg_piece_put<kRowsN>(slot, v, lane);
+      __syncwarp();
+      tg_piece_out(slot, out + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol > 0 ? 32 : 0, lane);
+    }
   } else {
-    // the pair (m2, m2 + 1) lies in the padded pitch even where m2 + 1 is past the matrix
-    const long long at = k.g * p.in_bs + (long long)(row0 + odd) * p.ldi + m2;
-    uint32_t hi[16], lo[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool in = 2 * i + odd < nrow;
-      hi[i] = in ? *reinterpret_cast<const uint32_t*>(p.in + at + 2 * i * p.ldi) : 0u;
-      lo[i] = in ? *reinterpret_cast<const uint32_t*>(p.lo + at + 2 * i * p.ldi) : 0u;
-    }
+    uint32_t lo[16];
+    tg_piece_get<kRowsN>(slot, v, lane);
+    tg_piece_get<kRowsN>(slot + kTgPiece, lo, lane);
     const float ca = alpha * p.ca, cb = alpha * p.cb;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (2 * i + odd >= nrow) break;
-      const float2 h = TgPair<__half>::unpack(hi[i]), l = TgPair<__half>::unpack(lo[i]);
-      const float a = ca * (h.x + l.x) + cb * __uint_as_float(r[2 * i]);
-      const float b = ca * (h.y + l.y) + cb * __uint_as_float(r[2 * i + 1]);
-      if (Epi == kTgUpdate) {
-        const uint32_t n = TgPair<__half>::pack(a, b);
-        const float2 nf = TgPair<__half>::unpack(n);
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<__half*>(p.out) + at + 2 * i * p.ldi) = n;
-        *reinterpret_cast<uint32_t*>(p.lo + at + 2 * i * p.ldi) = TgPair<__half>::pack(a - nf.x, b - nf.y);
-      } else {
-        bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)(row0 + 2 * i + odd) * p.ldo + m2;
-        if ((reinterpret_cast<uintptr_t>(o) & 3) == 0 && m2 + 1 < p.M) {
-          *reinterpret_cast<uint32_t*>(o) = TgPair<bf16>::pack(a, b);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
+        const float2 h = TgPair<__half>::unpack(v[4 * i + b]), l = TgPair<__half>::unpack(lo[4 * i + b]);
+        const float x = ca * (h.x + l.x) + cb * __uint_as_float(e[0]);
+        const float y = ca * (h.y + l.y) + cb * __uint_as_float(e[1]);
+        if (Epi == kTgUpdate) {
+          const uint32_t n = TgPair<__half>::pack(x, y);
+          const float2 nf = TgPair<__half>::unpack(n);
+          v[4 * i + b] = n;
+          lo[4 * i + b] = TgPair<__half>::pack(x - nf.x, y - nf.y);
         } else {
-          o[0] = __float2bfloat16(a);
-          if (m2 + 1 < p.M) o[1] = __float2bfloat16(b);
+          v[4 * i + b] = TgPair<bf16>::pack(x, y);
         }
       }
+    __syncwarp();
+    tg_piece_put<kRowsN>(slot, v, lane);
+    if (Epi == kTgUpdate) tg_piece_put<kRowsN>(slot + kTgPiece, lo, lane);
+    __syncwarp();
+    if (Epi == kTgUpdate) {
+      // whole pieces: the pitch is padded to 64
+      const long long at = k.g * p.in_bs + (long long)row0 * p.ldi + m;
+      const int cols = mcol > 0 ? 32 : 0;
+      tg_piece_out(slot, reinterpret_cast<__half*>(p.out) + at, p.ldi, nrow, cols, lane);
+      tg_piece_out(slot + kTgPiece, p.lo + at, p.ldi, nrow, cols, lane);
+    } else {
+      bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m;
+      if (p.ldo % 8 == 0 && p.M % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0)
+        tg_piece_out(slot, o, p.ldo, nrow, mcol, lane);
+      else
+        tg_piece_out_any(slot, reinterpret_cast<uint16_t*>(o), p.ldo, min(nrow, 32), mcol, lane);
     }
   }
-}
-
-// Symmetric outputs (A = X X^T and B = b A + c A A): the lane's 32 values are
-// 64 contiguous bytes of row m of the output (whose pitch is padded to 64, so
-// columns past the matrix may be written), and, off the diagonal, column m of
-// the 32 rows of the mirrored tile.
-template <int Epi>
-__device__ __forceinline__ void tg_emit_symmetric(const uint32_t (&r)[32], const TgParams& p, const TgTask& k, int row0,
-                                                  int nrow, int m, float alpha) {
-  if (m >= p.M) return;
-  __half* out = reinterpret_cast<__half*>(p.out) + k.g * p.out_bs;
-  const float cb = p.cb * alpha * alpha;
-  uint4 w[4];
-  if (Epi == kTgPoly) {
-    const uint4* in = reinterpret_cast<const uint4*>(p.in + k.g * p.in_bs + (long long)m * p.ldi + row0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = in[i];
-  }
-  uint32_t* v = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float a = cb * __uint_as_float(r[2 * i]), b = cb * __uint_as_float(r[2 * i + 1]);
-    if (Epi == kTgPoly) {
-      const float2 f = TgPair<__half>::unpack(v[i]);
-      a += p.ca * f.x;
-      b += p.ca * f.y;
-    }
-    v[i] = TgPair<__half>::pack(a, b);
-  }
-  uint4* at = reinterpret_cast<uint4*>(out + (long long)m * p.ldo + row0);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) at[i] = w[i];
-  if (k.m0 != k.n0) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < nrow)
-        reinterpret_cast<uint16_t*>(out)[(long long)(row0 + i) * p.ldo + m] =
-            (uint16_t)(i & 1 ? v[i >> 1] >> 16 : v[i >> 1]);
-  }
+  __syncwarp();   // the slot is free for the next input
 }
 
 template <int Mode, int Epi, typename T>
-__device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t tmem, uint32_t rank, int warp, int first, int step) {
+__device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32_t tmem, uint32_t rank, int warp,
+                            int first, int step) {
   const int lane = ptx::lane_id();
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t leader_empty0 = ptx::mapa(ptx::smem_u32(&s.acc_empty[0]), 0);
+  const bool reads = Epi == kTgPoly || Epi == kTgUpdate || Epi == kTgUpdateOut || (Epi == kTgStore && p.res != nullptr);
+  constexpr int kSlot = tg_planes<Epi>() * kTgPiece;
+  const uint32_t base = store + (warp - 4) * kSlot * (Epi == kTgStore && !reads ? 1 : 2);
+  int slot = 0;
   int acc = 0;
   uint32_t acc_phase = 0;
   for (int t = first; t < s.total; t += step) {
     const TgTask k = tg_decode<Mode>(t, p, s);
     const bool any = k.klen > 0;
-    if (any) {
-      bool ok = true;
-      if (lane == 0) ok = tg_wait(&s.acc_full[acc], acc_phase, p, s);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
-      ptx::tc_fence_after();
-    }
-    const int m = k.m0 + (int)rank * 128 + quad * 32 + lane;
-    float2 bias = make_float2(0.f, 0.f);
+    const int m = k.m0 + (int)rank * 128 + quad * 32;
+    if (reads && part * 32 < k.nt) tg_prefetch<Epi, T>(base + slot * kSlot, p, k, part, m, lane);
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
     float alpha = 1.f;
     if (Epi == kTgStore) {
-      if (p.bias != nullptr && (m & ~1) < p.M)
-        bias = TgPair<T>::unpack(*reinterpret_cast<const uint32_t*>(reinterpret_cast<const T*>(p.bias) + (m & ~1)));
+      if (p.bias != nullptr)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (m + 8 * b < p.M) bias[b] = (float)reinterpret_cast<const T*>(p.bias)[m + 8 * b + (lane >> 2)];
     } else if (p.alpha != nullptr) {
       alpha = p.alpha[k.g];
     }
+    if (any) {
+      if (!tg_wait_warp(&s.acc_full[acc], acc_phase, p, s)) break;
+      ptx::tc_fence_after();
+    }
     for (int c = part; c * 32 < k.nt; c += 2) {
-      uint32_t r[32];
-      __syncwarp();
+      uint32_t r[2][16];
       if (any) {
-        ptx::tmem_ld32(tmem + acc * 256 + c * 32 + ((uint32_t)(quad * 32) << 16), r);
-        ptx::tmem_ld_wait();
+        const uint32_t at = tmem + acc * 256 + c * 32 + ((uint32_t)(quad * 32) << 16);
+        tg_tmem_frag(at, r[0]);
+        tg_tmem_frag(at + (16u << 16), r[1]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = 0;
+        for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
       }
-      if (Epi == kTgGram || Epi == kTgPoly) tg_emit_symmetric<Epi>(r, p, k, k.n0 + c * 32, k.cols - c * 32, m, alpha);
-      else tg_emit_rows<Epi, T>(r, p, k, k.n0 + c * 32, k.cols - c * 32, m, lane, bias, alpha);
+      if (reads) {
+        if ((c + 2) * 32 < k.nt) {
+          tg_prefetch<Epi, T>(base + (slot ^ 1) * kSlot, p, k, c + 2, m, lane);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
+      }
+      if (any) ptx::tmem_ld_wait();
+      tg_piece<Epi, T>(base + slot * kSlot, r, p, k, c, m, lane, bias, alpha);
+      if (reads) slot ^= 1;
     }
     if (any) {
       ptx::tc_fence_before();
@@ -624,6 +783,7 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t tmem, uint32_
       }
     }
   }
+  ptx::cp_async_wait_all();
 }
 
 // ---------------------------------------------------------------- kernel
@@ -632,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
     moe_tile_gemm_kernel(const __grid_constant__ TgParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TgSmem& s = *reinterpret_cast<TgSmem*>(tiles + (size_t)p.stages * p.stage_bytes);
+  TgSmem& s = *reinterpret_cast<TgSmem*>(tiles + (size_t)p.stages * p.stage_bytes + p.epi_bytes);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -713,7 +873,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
   } else if (warp == 2) {
     tg_tail_warp<Mode>(p, s, tiles, rank, first, step);
   } else if (warp >= 4) {
-    tg_epilogue<Mode, Epi, T>(p, s, tmem, rank, warp, first, step);
+    tg_epilogue<Mode, Epi, T>(p, s, ptx::smem_u32(tiles) + p.stages * p.stage_bytes, tmem, rank, warp, first, step);
   }
   __syncwarp();
   ptx::tc_fence_before();
