@@ -14,11 +14,14 @@
 // is ever transposed in memory.
 //
 // Roles per CTA: warp 0 TMA loads, warp 1 MMA issue (leader CTA), warp 2 the
-// zero rows of a ragged reduction's last block, warp 3 TMEM, warps 4..11 the
-// epilogue. Each CTA loads its 128 rows of P and half of the tile's Q into its
+// zero rows of a ragged reduction's last block, warp 3 TMEM and the list of
+// tiles, warps 4..11 the epilogue. Each CTA loads its 128 rows of P and half of the tile's Q into its
 // own shared memory; both CTAs' bytes are counted on the leader's barrier.
 // Two TMEM accumulators let a tile's epilogue run under the next tile's MMAs.
-// Tiles are dealt round robin; nothing is exchanged between pairs.
+// Tiles are dealt round robin; nothing is exchanged between pairs. Warp 3 works
+// out each tile (up to six integer divisions, about 1200 cycles) up to four tiles ahead of the
+// others: in every role's own path this cost 2 us a tile, more than the MMAs of
+// a 256-row weight gradient.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -35,6 +38,7 @@ constexpr int kTgThreads = 384;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgMaxStages = 12;
 constexpr int kTgMaxGroups = 1024;
+constexpr int kTgRing = 4;               // tiles worked out ahead
 constexpr int kTgABytes = 128 * 128;     // 128 rows of P, 64 k each
 constexpr long long kTgTimeoutCycles = 4000000000ll;   // about two seconds
 
@@ -84,6 +88,15 @@ struct TgParams {
   int pdl;                  // launched with programmatic stream serialisation
 };
 
+struct TgTask {
+  int g;        // group or batch; -1: no more tiles
+  int m0;       // first M row of the tile
+  int n0;       // first N row of the tile (within Q; absolute in a ragged-N product)
+  int cols;     // valid N rows
+  int nt;       // MMA columns (multiple of 32)
+  int k0, klen; // reduction range
+};
+
 struct TgSmem {
   uint64_t full[kTgMaxStages];
   uint64_t empty[kTgMaxStages];
@@ -91,6 +104,9 @@ struct TgSmem {
   uint64_t peer_tail[kTgMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t task_full[kTgRing];
+  uint64_t task_empty[kTgRing];
+  TgTask task[kTgRing];
   uint32_t tmem_base;
   int abort;
   int total;
@@ -104,27 +120,31 @@ constexpr size_t tg_smem_bytes(int stages, int stage_bytes, int epi_bytes) {
   return 1024 + (size_t)stages * stage_bytes + epi_bytes + sizeof(TgSmem);
 }
 
-struct TgTask {
-  int g;        // group or batch
-  int m0;       // first M row of the tile
-  int n0;       // first N row of the tile (within Q; absolute in a ragged-N product)
-  int cols;     // valid N rows
-  int nt;       // MMA columns (multiple of 32)
-  int k0, klen; // reduction range
-};
-
 __device__ __forceinline__ void tg_set_error(const TgParams& p, TgSmem& s, int code, bool stop) {
   if (p.err != nullptr) atomicCAS(p.err, 0, code);
   if (stop) *reinterpret_cast<volatile int*>(&s.abort) = 1;
 }
 
 // Bounded wait on a local barrier phase, by one thread or by a whole warp (all
-// lanes poll; tg_wait_warp's answer is the same in every lane). The bound is on
-// SM cycles, which are cheap to read.
+// lanes poll; tg_wait_warp's answer is the same in every lane). The hint lets the
+// hardware suspend the warp for up to a millisecond per attempt: polling warps
+// cost power, which at full load is clock. The bound is on SM cycles, which are
+// cheap to read.
+__device__ __forceinline__ bool tg_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(ptx::smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, const TgParams& p, TgSmem& s) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  if (tg_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!ptx::mbar_try_wait(bar, parity)) {
+  while (!tg_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
     if (clock64() - t0 > kTgTimeoutCycles) {
       tg_set_error(p, s, kDevTimeout, true);
@@ -216,6 +236,47 @@ __device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, const TgSm
 // Reduction steps (of 16) of k block kb.
 __device__ __forceinline__ int tg_ksteps(const TgTask& k, int kb) { return min(4, (k.klen - kb * 64 + 15) >> 4); }
 
+// ---------------------------------------------------------------- list of tiles (warp 3)
+template <int Mode>
+__device__ void tg_schedule(const TgParams& p, TgSmem& s, int first, int step) {
+  int q = 0;
+  uint32_t phase = 0;
+  for (int t = first;; t += step) {
+    TgTask k{};
+    k.g = -1;
+    if (t < s.total) k = tg_decode<Mode>(t, p, s);
+    if (!tg_wait_warp(&s.task_empty[q], phase ^ 1, p, s)) return;
+    if (ptx::lane_id() == 0) {
+      s.task[q] = k;
+      ptx::mbar_arrive(&s.task_full[q]);
+    }
+    __syncwarp();
+    if (k.g < 0) return;
+    if (++q == kTgRing) {
+      q = 0;
+      phase ^= 1;
+    }
+  }
+}
+
+// A warp's place in the list.
+struct TgCursor {
+  int q = 0;
+  uint32_t phase = 0;
+  // The next tile; false at the end (or once a wait has been given up).
+  __device__ __forceinline__ bool next(TgTask& k, const TgParams& p, TgSmem& s) {
+    if (!tg_wait_warp(&s.task_full[q], phase, p, s)) return false;
+    k = s.task[q];
+    __syncwarp();
+    if (ptx::lane_id() == 0) ptx::mbar_arrive(&s.task_empty[q]);
+    if (++q == kTgRing) {
+      q = 0;
+      phase ^= 1;
+    }
+    return k.g >= 0;
+  }
+};
+
 // ---------------------------------------------------------------- loads
 __device__ __forceinline__ void tg_load3(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
   asm volatile(
@@ -267,12 +328,13 @@ __device__ __forceinline__ bool tg_has_tail(const TgTask& k, int kb) {
 }
 
 template <int Mode, bool PMn, bool QMn>
-__device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t rank, int first, int step) {
+__device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t rank) {
   int stage = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (int t = first; t < s.total && ok; t += step) {
-    const TgTask k = tg_decode<Mode>(t, p, s);
+  TgCursor list;
+  TgTask k;
+  while (ok && list.next(k, p, s)) {
     const int nk = (k.klen + 63) >> 6;
     const uint32_t tx = tg_stage_tx<QMn>(k);
     const int pbatch = Mode == kTgRaggedK ? 0 : k.g;
@@ -318,13 +380,13 @@ __device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32
 // last step are overwritten with zeros in both operands (zeros in one alone
 // would still meet an infinity or NaN of another group in the other).
 template <int Mode>
-__device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint32_t rank, int first, int step) {
-  if (Mode != kTgRaggedK) return;
+__device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint32_t rank) {
   const int lane = ptx::lane_id();
   int stage = 0;
   uint32_t used = 0;   // parity of each stage's tail barrier
-  for (int t = first; t < s.total; t += step) {
-    const TgTask k = tg_decode<Mode>(t, p, s);
+  TgCursor list;
+  TgTask k;
+  while (list.next(k, p, s)) {
     const int nk = (k.klen + 63) >> 6;
     if (nk == 0) continue;
     const int last = (stage + nk - 1) % p.stages;
@@ -357,7 +419,7 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint3
 // cycles to issue, more than its share of the tensor core's time (64 at 256
 // columns and two CTAs' operands).
 template <int Mode, bool PMn, bool QMn>
-__device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tmem, int first, int step) {
+__device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tmem) {
   const uint32_t fmt = p.f16 ? 0u : 1u;
   const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((PMn ? 1u : 0u) << 15) | ((QMn ? 1u : 0u) << 16) |
                           ((256u >> 4) << 24);
@@ -369,8 +431,9 @@ __device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tm
   uint32_t phase = 0;
   int acc = 0;
   uint32_t acc_phase = 0;
-  for (int t = first; t < s.total; t += step) {
-    const TgTask k = tg_decode<Mode>(t, p, s);
+  TgCursor list;
+  TgTask k;
+  while (list.next(k, p, s)) {
     const int nk = (k.klen + 63) >> 6;
     if (nk == 0) continue;
     if (!tg_wait_warp(&s.acc_empty[acc], acc_phase ^ 1, p, s)) return;
@@ -542,11 +605,12 @@ __device__ __forceinline__ void tg_piece_get(uint32_t piece, uint32_t (&v)[16], 
 __device__ __forceinline__ void tg_piece_out(uint32_t piece, void* g, long long ld, int rows, int cols, int lane) {
   const int c = lane & 3;
   uint16_t* at = reinterpret_cast<uint16_t*>(g) + (lane >> 2) * ld + c * 8;
+  uint4 w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = i * 8 + (lane >> 2);
-    if (row < rows && c * 8 < cols) *reinterpret_cast<uint4*>(at + i * 8 * ld) = tg_lds16(piece + tg_piece_at(row, c));
-  }
+  for (int i = 0; i < 4; ++i) w[i] = tg_lds16(piece + tg_piece_at(i * 8 + (lane >> 2), c));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 8 + (lane >> 2) < rows && c * 8 < cols) *reinterpret_cast<uint4*>(at + i * 8 * ld) = w[i];
 }
 __device__ __forceinline__ void tg_piece_in(uint32_t piece, const void* g, long long ld, int rows, int cols, int lane) {
   const int c = lane & 3;
@@ -604,13 +668,13 @@ __device__ __forceinline__ void tg_prefetch(uint32_t slot, const TgParams& p, co
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// One piece: r holds its accumulator, `slot` its shared memory (inputs landed).
-// m is the piece's first column of the output, bias[b] belongs to m + 8 b + lane / 4.
+// One piece, first half: from its accumulator r and its inputs in `slot` (landed)
+// to the packed result v (and lo, the lower half of X). m is the piece's first
+// column of the output, bias[b] belongs to m + 8 b + lane / 4.
 template <int Epi, typename T>
-__device__ __forceinline__ void tg_piece(uint32_t slot, uint32_t (&r)[2][16], const TgParams& p, const TgTask& k, int c,
-                                         int m, int lane, const float (&bias)[4], float alpha) {
-  const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
-  uint32_t v[16];
+__device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][16], uint32_t (&v)[16],
+                                               uint32_t (&lo)[16], const TgParams& p, const TgTask& k, int c, int m,
+                                               int lane, const float (&bias)[4], float alpha) {
   if (Epi == kTgStore) {
     uint32_t res[16];
     if (p.res != nullptr) tg_piece_get<kRowsN>(slot, res, lane);
@@ -623,11 +687,13 @@ __device__ __forceinline__ void tg_piece(uint32_t slot, uint32_t (&r)[2][16], co
         e[1] = __float_as_uint(__uint_as_float(e[1]) + bias[b]);
       }
     if (p.z != nullptr) {
+      const int row0 = k.n0 + c * 32;
       tg_pack<T>(r, v);
       __syncwarp();
       tg_piece_put<kRowsN>(slot, v, lane);
       __syncwarp();
-      tg_piece_out(slot, reinterpret_cast<T*>(p.z) + (long long)row0 * p.ldz + m, p.ldz, nrow, mcol, lane);
+      tg_piece_out(slot, reinterpret_cast<T*>(p.z) + (long long)row0 * p.ldz + m, p.ldz, k.cols - c * 32, p.M - m,
+                   lane);
     }
     tg_act_all(r, p.act);
     if (p.res != nullptr) {
@@ -642,14 +708,7 @@ __device__ __forceinline__ void tg_piece(uint32_t slot, uint32_t (&r)[2][16], co
         }
     }
     tg_pack<T>(r, v);
-    __syncwarp();
-    tg_piece_put<kRowsN>(slot, v, lane);
-    __syncwarp();
-    tg_piece_out(slot, reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol,
-                 lane);
   } else if (Epi == kTgGram || Epi == kTgPoly) {
-    // A = X X^T and B = b A + c A A are symmetric: the piece goes out as it lies (row m, whose pitch
-    // is padded to 64, so whole pieces fit) and, off the diagonal tiles, transposed to the mirrored place
     const float cb = p.cb * alpha * alpha;
     if (Epi == kTgPoly) tg_piece_get<kRowsM>(slot, v, lane);
 #pragma unroll
@@ -665,19 +724,7 @@ __device__ __forceinline__ void tg_piece(uint32_t slot, uint32_t (&r)[2][16], co
         }
         v[4 * i + b] = TgPair<__half>::pack(x, y);
       }
-    __half* out = reinterpret_cast<__half*>(p.out) + k.g * p.out_bs;
-    __syncwarp();
-    tg_piece_put<kRowsM>(slot, v, lane);
-    __syncwarp();
-    tg_piece_out(slot, out + (long long)m * p.ldo + row0, p.ldo, mcol, 32, lane);
-    if (k.m0 != k.n0) {
-      __syncwarp();
-      tg_piece_put<kRowsN>(slot, v, lane);
-      __syncwarp();
-      tg_piece_out(slot, out + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol > 0 ? 32 : 0, lane);
-    }
   } else {
-    uint32_t lo[16];
     tg_piece_get<kRowsN>(slot, v, lane);
     tg_piece_get<kRowsN>(slot + kTgPiece, lo, lane);
     const float ca = alpha * p.ca, cb = alpha * p.cb;
@@ -698,30 +745,58 @@ __device__ __forceinline__ void tg_piece(uint32_t slot, uint32_t (&r)[2][16], co
           v[4 * i + b] = TgPair<bf16>::pack(x, y);
         }
       }
-    __syncwarp();
+  }
+}
+
+// Second half: through `slot` to the output.
+template <int Epi, typename T>
+__device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v)[16], const uint32_t (&lo)[16],
+                                               const TgParams& p, const TgTask& k, int c, int m, int lane) {
+  const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
+  __syncwarp();
+  if (Epi == kTgStore) {
     tg_piece_put<kRowsN>(slot, v, lane);
-    if (Epi == kTgUpdate) tg_piece_put<kRowsN>(slot + kTgPiece, lo, lane);
     __syncwarp();
-    if (Epi == kTgUpdate) {
-      // whole pieces: the pitch is padded to 64
-      const long long at = k.g * p.in_bs + (long long)row0 * p.ldi + m;
-      const int cols = mcol > 0 ? 32 : 0;
-      tg_piece_out(slot, reinterpret_cast<__half*>(p.out) + at, p.ldi, nrow, cols, lane);
-      tg_piece_out(slot + kTgPiece, p.lo + at, p.ldi, nrow, cols, lane);
-    } else {
-      bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m;
-      if (p.ldo % 8 == 0 && p.M % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0)
-        tg_piece_out(slot, o, p.ldo, nrow, mcol, lane);
-      else
-        tg_piece_out_any(slot, reinterpret_cast<uint16_t*>(o), p.ldo, min(nrow, 32), mcol, lane);
+    tg_piece_out(slot, reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol,
+                 lane);
+  } else if (Epi == kTgGram || Epi == kTgPoly) {
+    // A = X X^T and B = b A + c A A are symmetric: the piece goes out as it lies (row m, whose pitch
+    // is padded to 64, so whole pieces fit) and, off the diagonal tiles, transposed to the mirrored place
+    __half* out = reinterpret_cast<__half*>(p.out) + k.g * p.out_bs;
+    tg_piece_put<kRowsM>(slot, v, lane);
+    __syncwarp();
+    tg_piece_out(slot, out + (long long)m * p.ldo + row0, p.ldo, mcol, 32, lane);
+    if (k.m0 != k.n0) {
+      __syncwarp();
+      tg_piece_put<kRowsN>(slot, v, lane);
+      __syncwarp();
+      tg_piece_out(slot, out + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol > 0 ? 32 : 0, lane);
     }
+  } else if (Epi == kTgUpdate) {
+    tg_piece_put<kRowsN>(slot, v, lane);
+    tg_piece_put<kRowsN>(slot + kTgPiece, lo, lane);
+    __syncwarp();
+    // whole pieces: the pitch is padded to 64
+    const long long at = k.g * p.in_bs + (long long)row0 * p.ldi + m;
+    const int cols = mcol > 0 ? 32 : 0;
+    tg_piece_out(slot, reinterpret_cast<__half*>(p.out) + at, p.ldi, nrow, cols, lane);
+    tg_piece_out(slot + kTgPiece, p.lo + at, p.ldi, nrow, cols, lane);
+  } else {
+    tg_piece_put<kRowsN>(slot, v, lane);
+    __syncwarp();
+    bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m;
+    if (p.ldo % 8 == 0 && p.M % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0)
+      tg_piece_out(slot, o, p.ldo, nrow, mcol, lane);
+    else
+      tg_piece_out_any(slot, reinterpret_cast<uint16_t*>(o), p.ldo, min(nrow, 32), mcol, lane);
   }
   __syncwarp();   // the slot is free for the next input
 }
 
-template <int Mode, int Epi, typename T>
-__device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32_t tmem, uint32_t rank, int warp,
-                            int first, int step) {
+// The accumulator of the next piece is on its way from TMEM while a piece is
+// stored, and the accumulator buffer is given back before the last one is.
+template <int Epi, typename T>
+__device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32_t tmem, uint32_t rank, int warp) {
   const int lane = ptx::lane_id();
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t leader_empty0 = ptx::mapa(ptx::smem_u32(&s.acc_empty[0]), 0);
@@ -731,8 +806,10 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
   int slot = 0;
   int acc = 0;
   uint32_t acc_phase = 0;
-  for (int t = first; t < s.total; t += step) {
-    const TgTask k = tg_decode<Mode>(t, p, s);
+  TgCursor list;
+  TgTask k, next;
+  bool more = list.next(k, p, s);
+  while (more) {
     const bool any = k.klen > 0;
     const int m = k.m0 + (int)rank * 128 + quad * 32;
     if (reads && part * 32 < k.nt) tg_prefetch<Epi, T>(base + slot * kSlot, p, k, part, m, lane);
@@ -746,22 +823,21 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
     } else if (p.alpha != nullptr) {
       alpha = p.alpha[k.g];
     }
+    uint32_t r[2][16];
+    const uint32_t from = tmem + acc * 256 + ((uint32_t)(quad * 32) << 16);
     if (any) {
       if (!tg_wait_warp(&s.acc_full[acc], acc_phase, p, s)) break;
       ptx::tc_fence_after();
-    }
-    for (int c = part; c * 32 < k.nt; c += 2) {
-      uint32_t r[2][16];
-      if (any) {
-        const uint32_t at = tmem + acc * 256 + c * 32 + ((uint32_t)(quad * 32) << 16);
-        tg_tmem_frag(at, r[0]);
-        tg_tmem_frag(at + (16u << 16), r[1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
+      if (part * 32 < k.nt) {
+        tg_tmem_frag(from + part * 32, r[0]);
+        tg_tmem_frag(from + part * 32 + (16u << 16), r[1]);
       }
+    }
+    more = list.next(next, p, s);
+    for (int c = part; c * 32 < k.nt; c += 2) {
+      const bool again = (c + 2) * 32 < k.nt;
       if (reads) {
-        if ((c + 2) * 32 < k.nt) {
+        if (again) {
           tg_prefetch<Epi, T>(base + (slot ^ 1) * kSlot, p, k, c + 2, m, lane);
           asm volatile("cp.async.wait_group 1;" ::: "memory");
         } else {
@@ -769,19 +845,34 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
         }
         __syncwarp();
       }
-      if (any) ptx::tmem_ld_wait();
-      tg_piece<Epi, T>(base + slot * kSlot, r, p, k, c, m, lane, bias, alpha);
+      if (any) {
+        ptx::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
+      }
+      uint32_t v[16], lo[16];
+      tg_piece_value<Epi, T>(base + slot * kSlot, r, v, lo, p, k, c, m, lane, bias, alpha);
+      if (any && again) {
+        tg_tmem_frag(from + (c + 2) * 32, r[0]);
+        tg_tmem_frag(from + (c + 2) * 32 + (16u << 16), r[1]);
+      }
+      if (any && !again) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
+      }
+      tg_piece_store<Epi, T>(base + slot * kSlot, v, lo, p, k, c, m, lane);
       if (reads) slot ^= 1;
     }
     if (any) {
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
+      if (part * 32 >= k.nt && lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
       }
     }
+    k = next;
   }
   ptx::cp_async_wait_all();
 }
@@ -807,6 +898,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s.acc_full[i], 1);
       ptx::mbar_init(&s.acc_empty[i], 2 * kTgEpiWarps);
+    }
+    for (int i = 0; i < kTgRing; ++i) {
+      ptx::mbar_init(&s.task_full[i], 1);
+      // readers: the producer, the leader's MMA warp, the tail warp of a ragged reduction, the epilogue
+      ptx::mbar_init(&s.task_empty[i], 1 + (rank == 0 ? 1 : 0) + (Mode == kTgRaggedK ? 1 : 0) + kTgEpiWarps);
     }
     s.abort = 0;
     ptx::fence_mbar_init();
@@ -867,13 +963,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 0) {
-    tg_producer<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), rank, first, step);
+    tg_producer<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), rank);
   } else if (warp == 1) {
-    if (rank == 0) tg_mma<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), tmem, first, step);
+    if (rank == 0) tg_mma<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), tmem);
   } else if (warp == 2) {
-    tg_tail_warp<Mode>(p, s, tiles, rank, first, step);
+    if (Mode == kTgRaggedK) tg_tail_warp<Mode>(p, s, tiles, rank);
+  } else if (warp == 3) {
+    tg_schedule<Mode>(p, s, first, step);
   } else if (warp >= 4) {
-    tg_epilogue<Mode, Epi, T>(p, s, ptx::smem_u32(tiles) + p.stages * p.stage_bytes, tmem, rank, warp, first, step);
+    tg_epilogue<Epi, T>(p, s, ptx::smem_u32(tiles) + p.stages * p.stage_bytes, tmem, rank, warp);
   }
   __syncwarp();
   ptx::tc_fence_before();
