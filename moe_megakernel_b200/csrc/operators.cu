@@ -1,7 +1,8 @@
 // C entry points of the operators around the MoE layer (include/moe_b200.h):
 // products grouped by expert, the dense layer and its backward, and the
 // orthogonalised update. Argument checks, tensor maps and launches; the
-// products run in tile_gemm.cuh, the element passes in operators.cuh.
+// products run in tile_gemm.cuh (few_rows.cuh for a few rows of one weight
+// matrix), the element passes in operators.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -12,6 +13,7 @@
 
 #include "../../include/moe_b200.h"
 #include "common.cuh"
+#include "few_rows.cuh"
 #include "operators.cuh"
 #include "tile_gemm.cuh"
 
@@ -91,9 +93,12 @@ void size_stages(TgParams& p, bool q_mn) {
 }
 
 // One launch. `tiles`: output tiles where the host knows them, else 0 (the
-// grid then covers every pair of SMs). Returns a moe_status.
+// grid then covers every pair of SMs). Launched with programmatic stream
+// serialisation: the kernel sets its barriers and TMEM up under the end of the
+// stream's previous kernel and waits for it before it reads or writes any
+// global memory. Returns a moe_status.
 template <int Mode, bool PMn, bool QMn, int Epi, typename T>
-int launch(TgParams& p, long long tiles, bool pdl, cudaStream_t st) {
+int launch(TgParams& p, long long tiles, cudaStream_t st) {
   static std::atomic<int> clusters[kMaxDevices];
   int sms = 0;
   const int d = current_device(&sms);
@@ -101,7 +106,7 @@ int launch(TgParams& p, long long tiles, bool pdl, cudaStream_t st) {
   if (sms < 0) return MOE_ERR_UNSUPPORTED_DEVICE;
   auto kernel = moe_tile_gemm_kernel<Mode, PMn, QMn, Epi, T>;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   cfg.blockDim = dim3(kTgThreads);
   cfg.stream = st;
   cfg.attrs = at;
@@ -115,14 +120,11 @@ int launch(TgParams& p, long long tiles, bool pdl, cudaStream_t st) {
     clusters[d].store(c);
   }
   size_stages<Epi>(p, QMn);
-  p.pdl = pdl ? 1 : 0;
   cfg.gridDim = dim3(2 * (unsigned)(tiles > 0 && tiles < c ? tiles : c));
   cfg.dynamicSmemBytes = tg_smem_bytes(p.stages, p.stage_bytes, p.epi_bytes);
-  if (pdl) {
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-  }
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -165,13 +167,87 @@ int ragged_tile(int rows, int groups) {
 
 template <bool PMn>
 int launch_rows(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
-  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedN, PMn, false, kTgStore, __half>(p, tiles, false, st)
-                                 : launch<kTgRaggedN, PMn, false, kTgStore, bf16>(p, tiles, false, st);
+  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedN, PMn, false, kTgStore, __half>(p, tiles, st)
+                                 : launch<kTgRaggedN, PMn, false, kTgStore, bf16>(p, tiles, st);
 }
 
 int launch_wgrad(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
-  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedK, true, true, kTgStore, __half>(p, tiles, false, st)
-                                 : launch<kTgRaggedK, true, true, kTgStore, bf16>(p, tiles, false, st);
+  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedK, true, true, kTgStore, __half>(p, tiles, st)
+                                 : launch<kTgRaggedK, true, true, kTgStore, bf16>(p, tiles, st);
+}
+
+// The cut of a few-rows product (few_rows.cuh) and its time in microseconds, and
+// the time of the same product on CTA pairs (tile_gemm.cuh). The figures are
+// fits to measured times of 8 to 120 MB of weights at 1 to 512 rows: a k block
+// (64 k of 128 features) takes a CTA 0.6 us when two run on every SM and W comes
+// from HBM, and a CTA 4.5 us besides (set-up, first load, joining the parts),
+// with 7 us more by 128 rows; a pair takes 0.27 us a k block of up to 240 columns
+// (its weight tile is 256 features) and 3 us besides, but its reduction is not
+// split. Measured, few rows / pairs: 14336 -> 4096 features, 37 rows 25 / 61 us;
+// 4096 -> 14336 24 / 24 us; 2048 -> 40000 43 / 36 us; 8192 -> 1024, 256 rows 17 / 37 us.
+struct FewCut {
+  int nt, split;
+  double us;
+};
+FewCut few_cut(int T, int M, int K, int sms) {
+  FewCut best{T <= 32 ? 32 : T <= 64 ? 64 : 128, 1, 1e30};
+  const long long cells = (long long)((M + 127) / 128) * ((T + best.nt - 1) / best.nt);
+  const int nk = (K + 63) / 64;
+  for (int c = 1; c <= kFewMaxSplit && c <= std::max(1, nk / 2); ++c) {
+    const double rounds = (double)((cells * c + 2 * sms - 1) / (2 * sms));
+    const double us = rounds * ((nk + c - 1) / c * 0.6 + 4.5 + 7.0 * std::min(T, 128) / 128);
+    if (us < best.us) best.split = c, best.us = us;
+  }
+  return best;
+}
+double pairs_us(long long tiles, int nt, int K, int pairs) {
+  return (double)((tiles + pairs - 1) / pairs) * ((K + 63) / 64 * std::max(0.27, nt * 0.0011) + 3.0);
+}
+
+template <bool PMn, typename T>
+int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Operand& Q, cudaStream_t st) {
+  static std::atomic<int> ready[kMaxDevices];
+  int d = -1;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return MOE_ERR_CUDA;
+  auto kernel = moe_few_rows_kernel<PMn, T>;
+  if (!ready[d].load()) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kFewSmemTiles + 1024 + sizeof(FewSmem))) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    ready[d].store(1);
+  }
+  FewParams f{};
+  f.M = p.M;
+  f.K = p.K;
+  f.T = p.N;
+  f.nt = cut.nt;
+  f.split = cut.split;
+  f.stages = std::min(kFewMaxStages, kFewSmemTiles / few_stage_bytes(f.nt));
+  f.f16 = p.f16;
+  f.err = p.err;
+  f.out = p.out;
+  f.ldo = p.ldo;
+  f.bias = p.bias;
+  f.res = p.res;
+  f.ldr = p.ldr;
+  f.z = p.z;
+  f.ldz = p.ldz;
+  f.act = p.act;
+  if (!map3(&f.tm_w, P, PMn ? 64 : 128, p.f16 != 0) || !map3(&f.tm_x, Q, f.nt, p.f16 != 0)) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = f.split;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = f.split > 1 ? 2 : 1;
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.gridDim = dim3((p.M + 127) / 128 * f.split, (p.N + f.nt - 1) / f.nt);
+  cfg.dynamicSmemBytes = few_smem_bytes(f.nt, f.stages);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, f) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // y = x W (transpose: x W^T) for one or several row groups; epilogue fields of p set by the caller.
@@ -198,6 +274,15 @@ int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int r
   const Operand P = transpose ? Operand{W, (uint64_t)K, (uint64_t)N, (uint64_t)K, (uint64_t)groups, (uint64_t)K * N}
                               : Operand{W, (uint64_t)N, (uint64_t)K, (uint64_t)N, (uint64_t)groups, (uint64_t)K * N};
   const Operand Q{x, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 1, 0};
+  if (p.offsets == nullptr && rows <= kFewMaxRows) {
+    if (sms < 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+    const FewCut cut = few_cut(rows, N, K, sms);
+    if (cut.us < pairs_us(tiles, p.nt, K, std::max(1, sms / 2))) {
+      if (dtype == MOE_DTYPE_FP16)
+        return transpose ? launch_few<false, __half>(p, cut, P, Q, st) : launch_few<true, __half>(p, cut, P, Q, st);
+      return transpose ? launch_few<false, bf16>(p, cut, P, Q, st) : launch_few<true, bf16>(p, cut, P, Q, st);
+    }
+  }
   if (!set_maps(p, P, !transpose, Q, false)) return MOE_ERR_CUDA;
   return transpose ? launch_rows<false>(p, dtype, tiles, st) : launch_rows<true>(p, dtype, tiles, st);
 }
@@ -456,8 +541,8 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g1.alpha = alpha;
     g1.cb = as / (xs * xs);
     if (!set_maps(g1, X, tall, X, tall)) return MOE_ERR_CUDA;
-    int rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(g1, tri, true, st)
-                  : launch<kTgSymmetric, false, false, kTgGram, __half>(g1, tri, true, st);
+    int rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(g1, tri, st)
+                  : launch<kTgSymmetric, false, false, kTgGram, __half>(g1, tri, st);
     if (rc) return rc;
     // B = b A + c A A
     TgParams g2 = g;
@@ -467,7 +552,7 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g2.ca = b;
     g2.cb = c / as;
     if (!set_maps(g2, A, false, A, false)) return MOE_ERR_CUDA;
-    if ((rc = launch<kTgSymmetric, false, false, kTgPoly, __half>(g2, tri, true, st))) return rc;
+    if ((rc = launch<kTgSymmetric, false, false, kTgPoly, __half>(g2, tri, st))) return rc;
     // X' = a X + B X: rows of X on the N side, its columns on the M side
     TgParams g3 = g;
     const bool last = i == steps - 1;
@@ -491,11 +576,11 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     const long long tiles = (long long)((m + g3.nt - 1) / g3.nt) * ((n + 255) / 256) * batch;
     if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (tall)
-      rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(g3, tiles, true, st)
-                : launch<kTgBatched, false, false, kTgUpdate, __half>(g3, tiles, true, st);
+      rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(g3, tiles, st)
+                : launch<kTgBatched, false, false, kTgUpdate, __half>(g3, tiles, st);
     else
-      rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(g3, tiles, true, st)
-                : launch<kTgBatched, true, false, kTgUpdate, __half>(g3, tiles, true, st);
+      rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(g3, tiles, st)
+                : launch<kTgBatched, true, false, kTgUpdate, __half>(g3, tiles, st);
     if (rc) return rc;
   }
   return MOE_OK;

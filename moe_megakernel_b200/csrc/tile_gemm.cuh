@@ -85,7 +85,6 @@ struct TgParams {
   long long ldi, in_bs;
   const float* alpha;       // [batches]: the first step's normalisation, or null
   float ca, cb;             // coefficients on the stored value and on the accumulator
-  int pdl;                  // launched with programmatic stream serialisation
 };
 
 struct TgTask {
@@ -913,10 +912,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
     ptx::tmem_alloc_pair(&s.tmem_base, kTmemCols);
     ptx::tmem_relinquish_pair();
   }
-  if (p.pdl) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the stream's earlier work is done and visible
 
   const int mt = (p.M + 255) >> 8;
   if (Mode == kTgRaggedN || Mode == kTgRaggedK) {

@@ -11,12 +11,11 @@ one element, receives the call's device error code (0 = none).
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from typing import Optional, Sequence, Union
 
 import torch
 
-from . import _ok, _ptr, _stream_handle, load_library
+from . import MoEError, load_library
 
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -33,6 +32,9 @@ def _tensor(t, name: str, dims: int):
 
 def _like(t, name: str, shape, dtype, device):
     """Shape, type and device of a tensor; its last index must be contiguous."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device
+            and (t.stride(-1) == 1 or shape[-1] <= 1)):
+        return
     _tensor(t, name, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -40,8 +42,7 @@ def _like(t, name: str, shape, dtype, device):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last index must be contiguous")
+    raise ValueError(f"{name}: the last index must be contiguous")
 
 
 def _whole(t, name: str, shape, dtype, device):
@@ -77,15 +78,30 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
+def _address(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _error_word(t, device):
     if t is not None:
         _whole(t, "error_word", (1,), torch.int32, device)
-    return _ptr(t)
+    return _address(t)
 
 
-def _on(device):
-    """The tensors' device as the current one for the call."""
-    return nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _raw_stream(stream, device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _call(name: str, device, *args):
+    """The C entry point `name`, with the tensors' device as the current one."""
+    f = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == device.index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args)
+    if rc:
+        raise MoEError(rc, name)
 
 
 def _workspace(nbytes: int, device, stream):
@@ -93,7 +109,9 @@ def _workspace(nbytes: int, device, stream):
     reused only by later work of that stream, and belongs to the graph when captured)."""
     if not nbytes:
         return None
-    with nullcontext() if stream is None else torch.cuda.stream(stream):
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
@@ -118,19 +136,19 @@ def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, tran
     _tensor(W, "W", 3)
     dt = _half(x, "x")
     rows, K = x.shape
-    groups = _offsets(offsets, x.device)
+    dev = x.device
+    groups = _offsets(offsets, dev)
     N = W.shape[1] if transpose else W.shape[2]
-    _like(x, "x", (rows, K), x.dtype, x.device)
-    _whole(W, "W", (groups, N, K) if transpose else (groups, K, N), x.dtype, x.device)
+    _like(x, "x", (rows, K), x.dtype, dev)
+    _whole(W, "W", (groups, N, K) if transpose else (groups, K, N), x.dtype, dev)
     _cuda(x, "x")
     if y is None:
-        y = torch.empty((rows, N), dtype=x.dtype, device=x.device)
-    _like(y, "y", (rows, N), x.dtype, x.device)
-    with _on(x.device):
-        _ok(load_library().moe_grouped_matmul(_ptr(x), _pitch(x, "x"), _ptr(W), _ptr(offsets), rows, groups, K, N,
-                                              1 if transpose else 0, dt, _ptr(y), _pitch(y, "y"),
-                                              _error_word(error_word, x.device), _stream_handle(stream, x.device)),
-            "moe_grouped_matmul")
+        y = torch.empty((rows, N), dtype=x.dtype, device=dev)
+    else:
+        _like(y, "y", (rows, N), x.dtype, dev)
+    _call("moe_grouped_matmul", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), offsets.data_ptr(), rows, groups, K, N,
+          1 if transpose else 0, dt, y.data_ptr(), _pitch(y, "y"), _error_word(error_word, dev),
+          _raw_stream(stream, dev))
     return y
 
 
@@ -144,18 +162,18 @@ def grouped_matmul_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tenso
     dt = _half(x, "x")
     rows, K = x.shape
     N = dy.shape[1]
-    groups = _offsets(offsets, x.device)
-    _like(x, "x", (rows, K), x.dtype, x.device)
-    _like(dy, "dy", (rows, N), x.dtype, x.device)
+    dev = x.device
+    groups = _offsets(offsets, dev)
+    _like(x, "x", (rows, K), x.dtype, dev)
+    _like(dy, "dy", (rows, N), x.dtype, dev)
     _cuda(x, "x")
     if dW is None:
-        dW = torch.empty((groups, K, N), dtype=x.dtype, device=x.device)
-    _whole(dW, "dW", (groups, K, N), x.dtype, x.device)
-    with _on(x.device):
-        _ok(load_library().moe_grouped_matmul_wgrad(_ptr(x), _pitch(x, "x"), _ptr(dy), _pitch(dy, "dy"), _ptr(offsets),
-                                                    rows, groups, K, N, dt, _ptr(dW),
-                                                    _error_word(error_word, x.device),
-                                                    _stream_handle(stream, x.device)), "moe_grouped_matmul_wgrad")
+        dW = torch.empty((groups, K, N), dtype=x.dtype, device=dev)
+    else:
+        _whole(dW, "dW", (groups, K, N), x.dtype, dev)
+    _call("moe_grouped_matmul_wgrad", dev, x.data_ptr(), _pitch(x, "x"), dy.data_ptr(), _pitch(dy, "dy"),
+          offsets.data_ptr(), rows, groups, K, N, dt, dW.data_ptr(), _error_word(error_word, dev),
+          _raw_stream(stream, dev))
     return dW
 
 
@@ -182,17 +200,16 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     _cuda(x, "x")
     if y is None:
         y = torch.empty((T, N), dtype=x.dtype, device=dev)
-    _like(y, "y", (T, N), x.dtype, dev)
-    if preact is None and save_preact:
-        preact = torch.empty((T, N), dtype=x.dtype, device=dev)
+    else:
+        _like(y, "y", (T, N), x.dtype, dev)
     if preact is not None:
         _like(preact, "preact", (T, N), x.dtype, dev)
-    with _on(dev):
-        _ok(load_library().moe_linear(_ptr(x), _pitch(x, "x"), _ptr(W), _ptr(bias), _ptr(residual),
-                                      0 if residual is None else _pitch(residual, "residual"), T, K, N, act, dt,
-                                      _ptr(y), _pitch(y, "y"), _ptr(preact),
-                                      0 if preact is None else _pitch(preact, "preact"),
-                                      _error_word(error_word, dev), _stream_handle(stream, dev)), "moe_linear")
+    elif save_preact:
+        preact = torch.empty((T, N), dtype=x.dtype, device=dev)
+    _call("moe_linear", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), _address(bias), _address(residual),
+          0 if residual is None else _pitch(residual, "residual"), T, K, N, act, dt, y.data_ptr(), _pitch(y, "y"),
+          _address(preact), 0 if preact is None else _pitch(preact, "preact"), _error_word(error_word, dev),
+          _raw_stream(stream, dev))
     return y if preact is None else (y, preact)
 
 
@@ -219,16 +236,14 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, preact: 
         _like(z, "preact", (T, N), x.dtype, dev)
     _cuda(x, "x")
     lib = load_library()
-    with _on(dev):
-        dx = torch.empty((T, K), dtype=x.dtype, device=dev) if input_grad else None
-        dW = torch.empty((K, N), dtype=x.dtype, device=dev) if weight_grad else None
-        dbias = torch.empty((N,), dtype=x.dtype, device=dev) if bias_grad else None
-        nbytes = lib.moe_linear_backward_workspace_bytes(T, N, act, 1 if bias_grad else 0)
-        ws = _workspace(nbytes, dev, stream)
-        _ok(lib.moe_linear_backward(_ptr(dy), _pitch(dy, "dy"), _ptr(x), _pitch(x, "x"), _ptr(W), _ptr(z),
-                                    0 if z is None else _pitch(z, "preact"), T, K, N, act, dt, _ptr(dx), K, _ptr(dW),
-                                    _ptr(dbias), _ptr(ws), nbytes, _error_word(error_word, dev),
-                                    _stream_handle(stream, dev)), "moe_linear_backward")
+    dx = torch.empty((T, K), dtype=x.dtype, device=dev) if input_grad else None
+    dW = torch.empty((K, N), dtype=x.dtype, device=dev) if weight_grad else None
+    dbias = torch.empty((N,), dtype=x.dtype, device=dev) if bias_grad else None
+    nbytes = lib.moe_linear_backward_workspace_bytes(T, N, act, 1 if bias_grad else 0)
+    ws = _workspace(nbytes, dev, stream)
+    _call("moe_linear_backward", dev, dy.data_ptr(), _pitch(dy, "dy"), x.data_ptr(), _pitch(x, "x"), W.data_ptr(),
+          _address(z), 0 if z is None else _pitch(z, "preact"), T, K, N, act, dt, _address(dx), K, _address(dW),
+          _address(dbias), _address(ws), nbytes, _error_word(error_word, dev), _raw_stream(stream, dev))
     return dict(dx=dx, dW=dW, dbias=dbias)
 
 
@@ -270,10 +285,9 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
     batch, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
     lib = load_library()
     flat = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
-    with _on(dev):
-        nbytes = lib.moe_orthogonalize_workspace_bytes(batch, m, n)
-        ws = _workspace(nbytes, dev, stream)
-        _ok(lib.moe_orthogonalize(_ptr(G), *pitches(G, "G"), batch, m, n, DTYPE_CODES[G.dtype], steps, flat, eps,
-                                  _ptr(out), *pitches(out, "out"), _ptr(ws), nbytes, _error_word(error_word, dev),
-                                  _stream_handle(stream, dev)), "moe_orthogonalize")
+    nbytes = lib.moe_orthogonalize_workspace_bytes(batch, m, n)
+    ws = _workspace(nbytes, dev, stream)
+    _call("moe_orthogonalize", dev, G.data_ptr(), *pitches(G, "G"), batch, m, n, DTYPE_CODES[G.dtype], steps, flat, eps,
+          out.data_ptr(), *pitches(out, "out"), _address(ws), nbytes, _error_word(error_word, dev),
+          _raw_stream(stream, dev))
     return out
