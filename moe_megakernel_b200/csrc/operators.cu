@@ -141,15 +141,18 @@ int clear_error_word(int32_t* err, cudaStream_t st) {
 }
 
 // N tile of a dense product of `rows` N-side rows and mt M tiles on `pairs` CTA
-// pairs: the multiple of 32 with the least (rounds of tiles) x (columns of a
-// tile + 32), the 32 standing for what a tile costs beside its MMAs.
-int pick_tile(long long rows, int mt, int batch, int pairs) {
+// pairs: the multiple of 32 with the least (rounds of tiles) x (256 + columns of
+// a tile that are loaded). A k block's time is its loads, 16 KB of P and 64
+// bytes a column of Q in each CTA, rather than its MMAs as soon as a tile is
+// below 256 columns; an MN-major Q is loaded in boxes of 64 columns in each CTA.
+int pick_tile(long long rows, int mt, int batch, int pairs, bool q_mn) {
   int best = 256;
   long long least = -1;
   for (int nt = 256; nt >= 32; nt -= 32) {
     const long long tiles = (rows + nt - 1) / nt;
     const long long each = ((rows + tiles - 1) / tiles + 31) / 32 * 32;
-    const long long cost = (tiles * mt * batch + pairs - 1) / pairs * (each + 32);
+    const long long loaded = q_mn ? (each + 127) / 128 * 128 : each;
+    const long long cost = (tiles * mt * batch + pairs - 1) / pairs * (256 + loaded);
     if (least < 0 || cost < least) {
       least = cost;
       best = (int)each;
@@ -265,7 +268,7 @@ int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int r
   const int mt = (N + 255) / 256;
   long long tiles = 0;
   if (p.offsets == nullptr) {
-    p.nt = pick_tile(rows, mt, 1, std::max(1, sms / 2));
+    p.nt = pick_tile(rows, mt, 1, std::max(1, sms / 2), false);
     tiles = (long long)((rows + p.nt - 1) / p.nt) * mt;
   } else {
     p.nt = ragged_tile(rows, groups);
@@ -301,7 +304,7 @@ int weight_gradient(TgParams& p, const void* x, long long ldx, const void* dy, l
   p.ldo = N;
   p.out_bs = (long long)K * N;
   const int mt = (N + 255) / 256;
-  p.nt = pick_tile(K, mt, groups, std::max(1, sms / 2));
+  p.nt = pick_tile(K, mt, groups, std::max(1, sms / 2), true);
   const long long tiles = (long long)((K + p.nt - 1) / p.nt) * mt * groups;
   if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const Operand P{dy, (uint64_t)N, (uint64_t)rows, (uint64_t)lddy, 1, 0};
@@ -452,8 +455,8 @@ extern "C" int moe_linear_backward(const void* dy, long long lddy, const void* x
     else moe_act_backward_kernel<bf16><<<grid, 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     if (dbias != nullptr) {
-      if (dtype == MOE_DTYPE_FP16) moe_bias_sum_kernel<__half><<<(N + 255) / 256, 256, 0, st>>>(a);
-      else moe_bias_sum_kernel<bf16><<<(N + 255) / 256, 256, 0, st>>>(a);
+      if (dtype == MOE_DTYPE_FP16) moe_bias_sum_kernel<__half><<<(N + 31) / 32, 256, 0, st>>>(a);
+      else moe_bias_sum_kernel<bf16><<<(N + 31) / 32, 256, 0, st>>>(a);
       if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
   }
@@ -559,7 +562,7 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g3.M = n;
     g3.N = m;
     g3.K = p0;
-    g3.nt = pick_tile(m, (n + 255) / 256, batch, pairs);
+    g3.nt = pick_tile(m, (n + 255) / 256, batch, pairs, false);
     g3.in = reinterpret_cast<const __half*>(ws + L.x[i & 1]);
     g3.lo = reinterpret_cast<__half*>(ws + L.lo);
     g3.ldi = L.ldx;

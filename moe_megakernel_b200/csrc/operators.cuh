@@ -28,57 +28,70 @@ struct ActParams {
 };
 
 // d act(z) / dz
-__device__ __forceinline__ float act_slope(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActGelu:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    case kActGeluTanh: {
-      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
-    }
-    case kActSilu: {
-      const float q = 1.f / (1.f + expf(-z));
-      return q * (1.f + z * (1.f - q));
-    }
-    default: return 1.f;
+template <int Act>
+__device__ __forceinline__ float act_slope(float z) {
+  if (Act == kActRelu) return z > 0.f ? 1.f : 0.f;
+  if (Act == kActGelu) {
+    float density;
+    const float phi = tg_normal(z, density);
+    return fmaf(z, density, phi);
   }
+  if (Act == kActGeluTanh) {
+    const float w = 0.044715f * z * z;
+    const float q = tg_sigmoid(1.59576912160573071f * fmaf(w, z, z));
+    return q * fmaf(z * (1.f - q) * 1.59576912160573071f, fmaf(3.f, w, 1.f), 1.f);
+  }
+  if (Act == kActSilu) {
+    const float q = tg_sigmoid(z);
+    return q * fmaf(z, 1.f - q, 1.f);
+  }
+  return 1.f;
 }
 
 // dz = dy act'(z), rounded once to the operand type of the two products that
 // read it, and this chunk's column sums of the unrounded dz.
+template <int Act, typename T>
+__device__ __forceinline__ void act_rows(const ActParams& p, int col, int first, int last, float (&acc)[8]) {
+  const T* dy = reinterpret_cast<const T*>(p.dy);
+  const T* z = reinterpret_cast<const T*>(p.z);
+  T* dz = reinterpret_cast<T*>(p.dz);
+#pragma unroll 2
+  for (int r = first; r < last; r += 8) {
+    const uint4 g = *reinterpret_cast<const uint4*>(dy + (long long)r * p.lddy + col);
+    uint4 v = g;
+    if (Act != kActNone) v = *reinterpret_cast<const uint4*>(z + (long long)r * p.ldz + col);
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, zw[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 d = TgPair<T>::unpack(gw[i]);
+      if (Act != kActNone) {
+        const float2 zf = TgPair<T>::unpack(zw[i]);
+        d.x *= act_slope<Act>(zf.x);
+        d.y *= act_slope<Act>(zf.y);
+      }
+      acc[2 * i] += d.x;
+      acc[2 * i + 1] += d.y;
+      o[i] = TgPair<T>::pack(d.x, d.y);
+    }
+    if (Act != kActNone) *reinterpret_cast<uint4*>(dz + (long long)r * p.N + col) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) moe_act_backward_kernel(const ActParams p) {
   __shared__ float sums[8][kActCols];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int col = blockIdx.x * kActCols + tx * 8;
-  const int r0 = blockIdx.y * p.rows, r1 = min(p.T, r0 + p.rows);
+  const int r0 = blockIdx.y * p.rows + ty, r1 = min(p.T, (int)(blockIdx.y + 1) * p.rows);
   float acc[8] = {};
   if (col < p.N) {   // N is a multiple of 8
-    const T* dy = reinterpret_cast<const T*>(p.dy);
-    const T* z = reinterpret_cast<const T*>(p.z);
-    T* dz = reinterpret_cast<T*>(p.dz);
-#pragma unroll 2
-    for (int r = r0 + ty; r < r1; r += 8) {
-      const uint4 g = *reinterpret_cast<const uint4*>(dy + (long long)r * p.lddy + col);
-      uint4 v = g;
-      if (p.act != kActNone) v = *reinterpret_cast<const uint4*>(z + (long long)r * p.ldz + col);
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, zw[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 d = TgPair<T>::unpack(gw[i]);
-        if (p.act != kActNone) {
-          const float2 zf = TgPair<T>::unpack(zw[i]);
-          d.x *= act_slope(zf.x, p.act);
-          d.y *= act_slope(zf.y, p.act);
-        }
-        acc[2 * i] += d.x;
-        acc[2 * i + 1] += d.y;
-        o[i] = TgPair<T>::pack(d.x, d.y);
-      }
-      if (p.dz != nullptr)
-        *reinterpret_cast<uint4*>(dz + (long long)r * p.N + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    switch (p.act) {
+      case kActRelu: act_rows<kActRelu, T>(p, col, r0, r1, acc); break;
+      case kActGelu: act_rows<kActGelu, T>(p, col, r0, r1, acc); break;
+      case kActGeluTanh: act_rows<kActGeluTanh, T>(p, col, r0, r1, acc); break;
+      case kActSilu: act_rows<kActSilu, T>(p, col, r0, r1, acc); break;
+      default: act_rows<kActNone, T>(p, col, r0, r1, acc);
     }
   }
   if (p.partial == nullptr) return;
@@ -94,14 +107,24 @@ __global__ void __launch_bounds__(256) moe_act_backward_kernel(const ActParams p
   }
 }
 
+// 32 columns a block, the chunks' sums over 8 warps.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_bias_sum_kernel(const ActParams p) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.N) return;
+  __shared__ float sums[8][32];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + tx;
   float v = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < p.chunks; ++i) v += p.partial[(long long)i * p.N + c];
-  reinterpret_cast<T*>(p.dbias)[c] = T(v);
+  if (c < p.N) {
+#pragma unroll 4
+    for (int i = ty; i < p.chunks; i += 8) v += p.partial[(long long)i * p.N + c];
+  }
+  sums[ty][tx] = v;
+  __syncthreads();
+  if (ty == 0 && c < p.N) {
+#pragma unroll
+    for (int y = 1; y < 8; ++y) v += sums[y][tx];
+    reinterpret_cast<T*>(p.dbias)[c] = T(v);
+  }
 }
 
 // ---------------------------------------------------------------- orthogonalize

@@ -489,12 +489,34 @@ struct TgPair<__half> {
   }
 };
 
+// Activations in some 15 instructions a value. The erf form takes Phi(z), the
+// normal distribution, from Abramowitz and Stegun 7.1.26 (1 - erf(x) =
+// t (a1 + t (a2 + ...)) e^(-x^2), t = 1 / (1 + p x), error below 1.5e-7), which
+// shares its exponential with the density that the backward needs; the tanh form
+// is z sigmoid(2 u). Errors stay near 1e-6 of the value, far below a 16-bit
+// rounding (2^-11). With erff the dense layer's backward pass spent 54 us in
+// 4093 x 7168 slopes, above the 27 us of their memory traffic.
+__device__ __forceinline__ float tg_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// Phi(z); density: e^(-z^2/2) / sqrt(2 pi)
+__device__ __forceinline__ float tg_normal(float z, float& density) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float e = __expf(-0.5f * z * z);
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                           0.254829592f);
+  const float tail = 0.5f * q * e;   // the smaller side
+  density = e * 0.39894228040143268f;
+  return z > 0.f ? 1.f - tail : tail;
+}
 template <int Act>
 __device__ __forceinline__ float tg_act(float z) {
   if (Act == kActRelu) return z > 0.f || z != z ? z : 0.f;
-  if (Act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (Act == kActGeluTanh) return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-  if (Act == kActSilu) return z / (1.f + expf(-z));
+  if (Act == kActGelu) {
+    float density;
+    return z * tg_normal(z, density);
+  }
+  if (Act == kActGeluTanh) return z * tg_sigmoid(1.59576912160573071f * fmaf(0.044715f * z * z, z, z));
+  if (Act == kActSilu) return z * tg_sigmoid(z);
   return z;
 }
 template <int Act>
