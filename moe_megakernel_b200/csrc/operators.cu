@@ -84,12 +84,14 @@ int current_device(int* num_sms) {
 }
 
 // Stages that fit beside the epilogue's pieces for the largest N tile (`nt`) of a launch.
-template <int Epi>
-void size_stages(TgParams& p, bool q_mn) {
+template <int Mode, int Epi>
+int size_stages(TgParams& p, bool q_mn) {
   const int half = p.nt / 2;
   p.stage_bytes = kTgABytes + (q_mn ? (half + 63) / 64 * 8192 : half * 128);
   p.epi_bytes = tg_epi_bytes<Epi>(p.res != nullptr);
-  p.stages = std::min(kTgMaxStages, (kTgSmemMax - (int)tg_smem_bytes(0, 0, p.epi_bytes)) / p.stage_bytes);
+  const int table = Mode == kTgRaggedN || Mode == kTgRaggedK ? p.groups : 0;
+  p.stages = std::min(kTgMaxStages, (kTgSmemMax - (int)tg_smem_bytes(0, 0, p.epi_bytes, table)) / p.stage_bytes);
+  return (int)tg_smem_bytes(p.stages, p.stage_bytes, p.epi_bytes, table);
 }
 
 // One launch. `tiles`: output tiles where the host knows them, else 0 (the
@@ -119,9 +121,9 @@ int launch(TgParams& p, long long tiles, cudaStream_t st) {
     if (cudaOccupancyMaxActiveClusters(&c, kernel, &cfg) != cudaSuccess || c < 1) return MOE_ERR_CUDA;
     clusters[d].store(c);
   }
-  size_stages<Epi>(p, QMn);
+  const int bytes = size_stages<Mode, Epi>(p, QMn);
   cfg.gridDim = dim3(2 * (unsigned)(tiles > 0 && tiles < c ? tiles : c));
-  cfg.dynamicSmemBytes = tg_smem_bytes(p.stages, p.stage_bytes, p.epi_bytes);
+  cfg.dynamicSmemBytes = bytes;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
@@ -322,7 +324,7 @@ size_t dz_bytes(int T, int N) { return up((size_t)T * N * 2, 256); }
 // ---- orthogonalize workspace
 struct OrthoLayout {
   size_t x[2], lo, a, b, partial, alpha, total;
-  long long ldx, lda, bsx, bsa;
+  long long ldx, lda, bsx, bsa, bsl;
 };
 OrthoLayout ortho_layout(int batch, int m, int n) {
   OrthoLayout L{};
@@ -331,6 +333,7 @@ OrthoLayout ortho_layout(int batch, int m, int n) {
   L.lda = (long long)up(p, 64);
   L.bsx = L.ldx * m;
   L.bsa = L.lda * p;
+  L.bsl = L.ldx * (long long)up(m, 32);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -339,7 +342,7 @@ OrthoLayout ortho_layout(int batch, int m, int n) {
   };
   L.x[0] = take((size_t)batch * L.bsx * 2);
   L.x[1] = take((size_t)batch * L.bsx * 2);
-  L.lo = take((size_t)batch * L.bsx * 2);
+  L.lo = take((size_t)batch * L.bsl);
   L.a = take((size_t)batch * L.bsa * 2);
   L.b = take((size_t)batch * L.bsa * 2);
   L.partial = take((size_t)batch * kOrthoChunks * 8);
@@ -508,16 +511,16 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
   const float xs = (float)(1 << s), as = 1024.f;   // A and B are stored times 2^10
 
   OrthoParams o{G, ldg, bsg, m, n, xs, eps, reinterpret_cast<double*>(ws + L.partial),
-                reinterpret_cast<float*>(ws + L.alpha), reinterpret_cast<__half*>(ws + L.x[0]),
-                reinterpret_cast<__half*>(ws + L.lo), L.ldx, L.bsx,
-                (int)std::min<long long>(kOrthoChunks, ((long long)m * n + 8191) / 8192)};
+                reinterpret_cast<float*>(ws + L.alpha), reinterpret_cast<__half*>(ws + L.x[0]), ws + L.lo, L.ldx, L.bsx,
+                L.bsl, (int)std::min<long long>(kOrthoChunks, ((long long)m * n + 4095) / 4096)};
+  const bool fp32 = dtype == MOE_DTYPE_FP32;
   const dim3 grid(o.chunks, batch);
-  if (dtype == MOE_DTYPE_FP32) {
+  if (fp32) {
     moe_ortho_norm_kernel<float><<<grid, 256, 0, st>>>(o);
-    moe_ortho_scale_kernel<float><<<grid, 256, 0, st>>>(o);
+    moe_ortho_scale_fp32_kernel<<<grid, 256, 0, st>>>(o);
   } else {
     moe_ortho_norm_kernel<bf16><<<grid, 256, 0, st>>>(o);
-    moe_ortho_scale_kernel<bf16><<<grid, 256, 0, st>>>(o);
+    moe_ortho_scale_bf16_kernel<<<grid, 256, 0, st>>>(o);
   }
   if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
 
@@ -543,6 +546,7 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g1.out = ws + L.a;
     g1.alpha = alpha;
     g1.cb = as / (xs * xs);
+    g1.backwards = 1;   // from the batches that the step before wrote last, which L2 still holds
     if (!set_maps(g1, X, tall, X, tall)) return MOE_ERR_CUDA;
     int rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(g1, tri, st)
                   : launch<kTgSymmetric, false, false, kTgGram, __half>(g1, tri, st);
@@ -564,7 +568,9 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g3.K = p0;
     g3.nt = pick_tile(m, (n + 255) / 256, batch, pairs, false);
     g3.in = reinterpret_cast<const __half*>(ws + L.x[i & 1]);
-    g3.lo = reinterpret_cast<__half*>(ws + L.lo);
+    g3.lo_in = i == 0 && !fp32 ? nullptr : ws + L.lo;   // a scaled bf16 gradient needs none
+    g3.lo_out = ws + L.lo;
+    g3.lo_bs = L.bsl;
     g3.ldi = L.ldx;
     g3.in_bs = L.bsx;
     g3.alpha = alpha;

@@ -136,8 +136,8 @@ struct OrthoParams {
   double* partial;   // [batch, kOrthoChunks]
   float* alpha;      // [batch]
   __half* hi;
-  __half* lo;
-  long long ldx, bsx;
+  uint8_t* lo;       // fp32 gradients only, in pieces (tg_low_at's order)
+  long long ldx, bsx, lo_bs;
   int chunks;
 };
 
@@ -198,8 +198,15 @@ __global__ void __launch_bounds__(256) moe_ortho_norm_kernel(const OrthoParams p
       for (int c = tx; c < items; c += lanes) {
         float v[8];
         ortho_load8(row + c * 8, v);
+        float s8 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc += (double)v[i] * v[i];
+        for (int i = 0; i < 8; ++i) s8 = fmaf(v[i], v[i], s8);
+        if (s8 > 1e-30f && s8 < 1e37f) {   // eight squares in fp32 where they stay normal numbers
+          acc += s8;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc += (double)v[i] * v[i];
+        }
       }
     } else {
 #pragma unroll 4
@@ -213,53 +220,88 @@ __global__ void __launch_bounds__(256) moe_ortho_norm_kernel(const OrthoParams p
   if (threadIdx.x == 0) p.partial[blockIdx.y * kOrthoChunks + blockIdx.x] = s;
 }
 
-// X0 = G / (|G| + eps) as two factors: G times a power of two, exact up to the
-// width of the fp16 pair (upper half hi, remainder lo: 22 bits), and
-// alpha = 2^E / (|G| + eps), which the first step's epilogues apply in fp32.
-template <typename T>
-__global__ void __launch_bounds__(256) moe_ortho_scale_kernel(const OrthoParams p) {
-  __shared__ double scratch[8];
+// X0 = G / (|G| + eps) as two factors: G times a power of two (exact in fp16 for
+// a bf16 gradient down to 2^-17 of the scale, with 8 bits more for an fp32 one),
+// and alpha = 2^E / (|G| + eps), which the first step's epilogues apply in fp32.
+__device__ __forceinline__ double ortho_scale(const OrthoParams& p, double* scratch) {
   const double total =
       block_sum(threadIdx.x < p.chunks ? p.partial[blockIdx.y * kOrthoChunks + threadIdx.x] : 0.0, scratch);
   const double norm = sqrt(total);
   const int e = norm > 0 && norm < 1e300 ? ilogb(norm) : 0;
-  const double scale = ldexp((double)p.xs, -e);
   if (blockIdx.x == 0 && threadIdx.x == 0)
     p.alpha[blockIdx.y] = norm > 0 ? (float)(ldexp(1.0, e) / (norm + p.eps)) : norm == 0 ? 0.f : (float)norm;
-  const T* g = reinterpret_cast<const T*>(p.g) + blockIdx.y * p.bsg;
+  return ldexp((double)p.xs, -e);
+}
+
+__global__ void __launch_bounds__(256) moe_ortho_scale_bf16_kernel(const OrthoParams p) {
+  __shared__ double scratch[8];
+  const double scale = ortho_scale(p, scratch);
+  const bf16* g = reinterpret_cast<const bf16*>(p.g) + blockIdx.y * p.bsg;
   __half* hi = p.hi + blockIdx.y * p.bsx;
-  __half* lo = p.lo + blockIdx.y * p.bsx;
-  const bool wide = ortho_wide<T>(p);
+  const bool wide = ortho_wide<bf16>(p);
   const int items = wide ? p.n / 8 : p.n;
   const int lanes = ortho_lanes(items);
   const int tx = threadIdx.x & (lanes - 1), ty = threadIdx.x / lanes, rows = 256 / lanes;
   for (int r = blockIdx.x * rows + ty; r < p.m; r += gridDim.x * rows) {
-    const T* row = g + (long long)r * p.ldg;
+    const bf16* row = g + (long long)r * p.ldg;
     if (wide) {
-#pragma unroll 2
+#pragma unroll 4
       for (int c = tx; c < items; c += lanes) {
         float v[8];
         ortho_load8(row + c * 8, v);
-        uint32_t h[4], l[4];
+        uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = (float)(v[2 * i] * scale), b = (float)(v[2 * i + 1] * scale);
-          h[i] = TgPair<__half>::pack(a, b);
-          const float2 f = TgPair<__half>::unpack(h[i]);
-          l[i] = TgPair<__half>::pack(a - f.x, b - f.y);
-        }
+        for (int i = 0; i < 4; ++i) h[i] = TgPair<__half>::pack((float)(v[2 * i] * scale), (float)(v[2 * i + 1] * scale));
         *reinterpret_cast<uint4*>(hi + (long long)r * p.ldx + c * 8) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + (long long)r * p.ldx + c * 8) = make_uint4(l[0], l[1], l[2], l[3]);
       }
     } else {
 #pragma unroll 4
-      for (int c = tx; c < items; c += lanes) {
-        const float a = (float)(ortho_value(row + c) * scale);
-        const __half h = __float2half_rn(a);
-        hi[(long long)r * p.ldx + c] = h;
-        lo[(long long)r * p.ldx + c] = __float2half_rn(a - __half2float(h));
-      }
+      for (int c = tx; c < items; c += lanes)
+        hi[(long long)r * p.ldx + c] = __float2half_rn((float)(ortho_value(row + c) * scale));
     }
+  }
+}
+
+// fp32: a warp turns 32 x 32 pieces into the update epilogue's order.
+__global__ void __launch_bounds__(256) moe_ortho_scale_fp32_kernel(const OrthoParams p) {
+  __shared__ double scratch[8];
+  __shared__ __align__(128) uint8_t stage[8][kTgPiece];
+  const double scale = ortho_scale(p, scratch);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t piece = ptx::smem_u32(stage[warp]);
+  const float* g = reinterpret_cast<const float*>(p.g) + blockIdx.y * p.bsg;
+  __half* hi = p.hi + blockIdx.y * p.bsx;
+  uint8_t* lo = p.lo + blockIdx.y * p.lo_bs;
+  const int across = (p.n + 31) / 32, pieces = across * ((p.m + 31) / 32);
+  for (int at = blockIdx.x * 8 + warp; at < pieces; at += gridDim.x * 8) {
+    const int r0 = at / across * 32, c0 = (at - at / across * across) * 32;
+    float f[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {   // value j: 8 x 8 block j / 2 (n block j / 8, m block j / 2 % 4), row parity j % 2
+      const int row = r0 + 8 * (j >> 3) + 2 * (lane & 3) + (j & 1), col = c0 + 8 * ((j >> 1) & 3) + (lane >> 2);
+      f[j] = row < p.m && col < p.n ? g[(long long)row * p.ldg + col] : 0.f;
+    }
+    uint32_t v[16], w[8];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      int q[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x = (float)(f[j + 2 * h] * scale), y = (float)(f[j + 2 * h + 1] * scale);
+        v[(j >> 1) + h] = TgPair<__half>::pack(x, y);
+        const float2 n = TgPair<__half>::unpack(v[(j >> 1) + h]);
+        q[2 * h] = tg_low(x, n.x);
+        q[2 * h + 1] = tg_low(y, n.y);
+      }
+      w[j >> 2] = tg_low4(q[0], q[1], q[2], q[3]);
+    }
+    uint4* out = reinterpret_cast<uint4*>(lo + ((long long)(r0 >> 5) * (p.ldx >> 5) + (c0 >> 5)) * 1024 + lane * 32);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    __syncwarp();
+    tg_piece_put<kRowsN>(piece, v, lane);
+    __syncwarp();
+    tg_piece_out(piece, hi + (long long)r0 * p.ldx + c0, p.ldx, p.m - r0, 32, lane);
   }
 }
 

@@ -80,11 +80,13 @@ struct TgParams {
   long long ldz;
   int act;
   // Newton-Schulz
-  const __half* in;         // kTgPoly: A; kTgUpdate: X, upper half
-  __half* lo;               // kTgUpdate: X, lower half (read, then written)
-  long long ldi, in_bs;
+  const __half* in;         // kTgPoly: A; kTgUpdate: X, the fp16 part
+  const uint8_t* lo_in;     // kTgUpdate: X, the 8 bits below it, in pieces (null: none)
+  uint8_t* lo_out;
+  long long ldi, in_bs, lo_bs;
   const float* alpha;       // [batches]: the first step's normalisation, or null
   float ca, cb;             // coefficients on the stored value and on the accumulator
+  int backwards;            // batches from the last to the first
 };
 
 struct TgTask {
@@ -109,14 +111,16 @@ struct TgSmem {
   uint32_t tmem_base;
   int abort;
   int total;
-  int start[kTgMaxGroups + 1];   // group offsets as used (an invalid group is empty)
-  int count[kTgMaxGroups];
-  int tile0[kTgMaxGroups + 1];   // first N tile of each group (ragged N)
+  // behind it, in ragged products: start[groups] and count[groups], the groups' rows as used (an
+  // invalid group is empty), and tile0[groups + 1], the first N tile of each group (ragged N)
+  __device__ int* start() { return reinterpret_cast<int*>(this + 1); }
+  __device__ int* count(int groups) { return start() + groups; }
+  __device__ int* tile0(int groups) { return start() + 2 * groups; }
 };
 
 constexpr int kTgSmemMax = 232448;   // shared memory of a CTA
-constexpr size_t tg_smem_bytes(int stages, int stage_bytes, int epi_bytes) {
-  return 1024 + (size_t)stages * stage_bytes + epi_bytes + sizeof(TgSmem);
+constexpr size_t tg_smem_bytes(int stages, int stage_bytes, int epi_bytes, int table_groups) {
+  return 1024 + (size_t)stages * stage_bytes + epi_bytes + sizeof(TgSmem) + (3 * (size_t)table_groups + 1) * 4;
 }
 
 __device__ __forceinline__ void tg_set_error(const TgParams& p, TgSmem& s, int code, bool stop) {
@@ -186,22 +190,23 @@ __device__ __forceinline__ void tg_split(int rows, int cap, int j, int& at, int&
 }
 
 template <int Mode>
-__device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, const TgSmem& s) {
+__device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, TgSmem& s) {
   TgTask k{};
   const int mt = (p.M + 255) >> 8;
   if (Mode == kTgRaggedN) {
+    const int* tile0 = s.tile0(p.groups);
     int lo = 0, hi = p.groups - 1;   // the last group whose first tile is at or before t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (s.tile0[mid] * mt <= t) lo = mid;
+      if (tile0[mid] * mt <= t) lo = mid;
       else hi = mid - 1;
     }
     k.g = lo;
-    const int ntl = s.tile0[lo + 1] - s.tile0[lo];
+    const int ntl = tile0[lo + 1] - tile0[lo];
     int m, n;
-    tg_raster(t - s.tile0[lo] * mt, mt, ntl, m, n);
-    tg_split(s.count[lo], p.nt, n, k.n0, k.cols);
-    k.n0 += s.start[lo];
+    tg_raster(t - tile0[lo] * mt, mt, ntl, m, n);
+    tg_split(s.count(p.groups)[lo], p.nt, n, k.n0, k.cols);
+    k.n0 += s.start()[lo];
     k.m0 = m << 8;
     k.k0 = 0;
     k.klen = p.K;
@@ -222,12 +227,13 @@ __device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, const TgSm
     tg_split(p.N, p.nt, n, k.n0, k.cols);
     k.m0 = m << 8;
     if (Mode == kTgRaggedK) {
-      k.k0 = s.start[k.g];
-      k.klen = s.count[k.g];
+      k.k0 = s.start()[k.g];
+      k.klen = s.count(p.groups)[k.g];
     } else {
       k.klen = p.K;
     }
   }
+  if ((Mode == kTgBatched || Mode == kTgSymmetric) && p.backwards) k.g = p.groups - 1 - k.g;
   k.nt = (k.cols + 31) & ~31;
   return k;
 }
@@ -662,14 +668,33 @@ __device__ __forceinline__ void tg_pack(const uint32_t (&r)[2][16], uint32_t (&v
                                      __uint_as_float(r[b >> 1][4 * i + 2 * (b & 1) + 1]));
 }
 
-// Pieces a warp keeps in shared memory: two slots when the epilogue reads (the
-// next piece's input is on its way while this one is worked on), each of one
-// plane, or two where X comes as a pair.
+// Pieces a warp keeps in shared memory: all four of its share of a tile when the
+// epilogue reads, so that a tile's whole input is on its way before its MMAs end
+// (with two, the wait for each third and fourth piece took longer than the piece).
 template <int Epi>
-__host__ __device__ constexpr int tg_planes() { return Epi == kTgUpdate || Epi == kTgUpdateOut ? 2 : 1; }
+__host__ __device__ constexpr int tg_slots(bool residual) { return Epi == kTgGram || (Epi == kTgStore && !residual) ? 1 : 4; }
 template <int Epi>
-__host__ __device__ constexpr int tg_epi_bytes(bool residual) {
-  return kTgEpiWarps * tg_planes<Epi>() * kTgPiece * (Epi == kTgStore && !residual ? 1 : 2);
+__host__ __device__ constexpr int tg_epi_bytes(bool residual) { return kTgEpiWarps * kTgPiece * tg_slots<Epi>(residual); }
+
+// X is carried as an fp16 value, which the products read, and 8 bits more: the
+// difference of the fp32 pattern from the fp16 value's, in units of 2^-18 of the
+// value. Together 19 bits, so that a X keeps small singular directions beside
+// large ones at 3 bytes an entry. The 8 bits never leave this epilogue and lie
+// in the order its threads hold them: a piece is 32 lanes x 32 bytes.
+__device__ __forceinline__ int tg_low(float x, float h) {
+  const int d = (__float_as_int(x) - __float_as_int(h)) >> 5;
+  return max(-128, min(127, d));
+}
+// hi: two fp16 of which byte pair `half` of w is the low part
+__device__ __forceinline__ float2 tg_wide(uint32_t hi, uint32_t w, int half) {
+  const float2 f = TgPair<__half>::unpack(hi);
+  int a, b;   // bytes 0 and 1 (2 and 3), sign-extended (bit 3 of a selector repeats the byte's sign)
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(a) : "r"(w), "r"(half ? 0xaaa2 : 0x8880));
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(b) : "r"(w), "r"(half ? 0xbbb3 : 0x9991));
+  return make_float2(__int_as_float(__float_as_int(f.x) + a * 32), __int_as_float(__float_as_int(f.y) + b * 32));
+}
+__device__ __forceinline__ uint32_t tg_low4(int a, int b, int c, int d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 template <int Epi, typename T>
@@ -681,12 +706,14 @@ __device__ __forceinline__ void tg_prefetch(uint32_t slot, const TgParams& p, co
     } else if (Epi == kTgPoly) {   // rows of A (m), whose pitch reaches past the last column
       tg_piece_in(slot, p.in + k.g * p.in_bs + (long long)m * p.ldi + row0, p.ldi, mcol, 32, lane);
     } else if (Epi == kTgUpdate || Epi == kTgUpdateOut) {
-      const long long at = k.g * p.in_bs + (long long)row0 * p.ldi + m;
-      tg_piece_in(slot, p.in + at, p.ldi, nrow, 32, lane);
-      tg_piece_in(slot + kTgPiece, p.lo + at, p.ldi, nrow, 32, lane);
+      tg_piece_in(slot, p.in + k.g * p.in_bs + (long long)row0 * p.ldi + m, p.ldi, nrow, 32, lane);
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// The low bits of one piece (k.n0 and m are multiples of 32).
+__device__ __forceinline__ long long tg_low_at(const TgParams& p, const TgTask& k, int c, int m, int lane) {
+  return k.g * p.lo_bs + ((long long)((k.n0 >> 5) + c) * (p.ldi >> 5) + (m >> 5)) * 1024 + lane * 32;
 }
 
 // One piece, first half: from its accumulator r and its inputs in `slot` (landed)
@@ -694,7 +721,7 @@ __device__ __forceinline__ void tg_prefetch(uint32_t slot, const TgParams& p, co
 // column of the output, bias[b] belongs to m + 8 b + lane / 4.
 template <int Epi, typename T>
 __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][16], uint32_t (&v)[16],
-                                               uint32_t (&lo)[16], const TgParams& p, const TgTask& k, int c, int m,
+                                               uint32_t (&lo)[8], const TgParams& p, const TgTask& k, int c, int m,
                                                int lane, const float (&bias)[4], float alpha) {
   if (Epi == kTgStore) {
     uint32_t res[16];
@@ -747,31 +774,34 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
       }
   } else {
     tg_piece_get<kRowsN>(slot, v, lane);
-    tg_piece_get<kRowsN>(slot + kTgPiece, lo, lane);
     const float ca = alpha * p.ca, cb = alpha * p.cb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 16; j += 2) {   // two 8 x 8 blocks: four values, one word of low bits
+      int q[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int h = 0; h < 2; ++h) {
+        const int i = (j + h) >> 2, b = (j + h) & 3;
         const uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
-        const float2 h = TgPair<__half>::unpack(v[4 * i + b]), l = TgPair<__half>::unpack(lo[4 * i + b]);
-        const float x = ca * (h.x + l.x) + cb * __uint_as_float(e[0]);
-        const float y = ca * (h.y + l.y) + cb * __uint_as_float(e[1]);
+        const float2 old = tg_wide(v[j + h], lo[j >> 1], h);
+        const float x = ca * old.x + cb * __uint_as_float(e[0]);
+        const float y = ca * old.y + cb * __uint_as_float(e[1]);
         if (Epi == kTgUpdate) {
-          const uint32_t n = TgPair<__half>::pack(x, y);
-          const float2 nf = TgPair<__half>::unpack(n);
-          v[4 * i + b] = n;
-          lo[4 * i + b] = TgPair<__half>::pack(x - nf.x, y - nf.y);
+          v[j + h] = TgPair<__half>::pack(x, y);
+          const float2 n = TgPair<__half>::unpack(v[j + h]);
+          q[2 * h] = tg_low(x, n.x);
+          q[2 * h + 1] = tg_low(y, n.y);
         } else {
-          v[4 * i + b] = TgPair<bf16>::pack(x, y);
+          v[j + h] = TgPair<bf16>::pack(x, y);
         }
       }
+      if (Epi == kTgUpdate) lo[j >> 1] = tg_low4(q[0], q[1], q[2], q[3]);
+    }
   }
 }
 
 // Second half: through `slot` to the output.
 template <int Epi, typename T>
-__device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v)[16], const uint32_t (&lo)[16],
+__device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v)[16], const uint32_t (&lo)[8],
                                                const TgParams& p, const TgTask& k, int c, int m, int lane) {
   const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
   __syncwarp();
@@ -794,14 +824,16 @@ __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v
       tg_piece_out(slot, out + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol > 0 ? 32 : 0, lane);
     }
   } else if (Epi == kTgUpdate) {
+    if (mcol > 0 && nrow > 0) {
+      uint4* at = reinterpret_cast<uint4*>(p.lo_out + tg_low_at(p, k, c, m, lane));
+      at[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      at[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    }
     tg_piece_put<kRowsN>(slot, v, lane);
-    tg_piece_put<kRowsN>(slot + kTgPiece, lo, lane);
     __syncwarp();
     // whole pieces: the pitch is padded to 64
-    const long long at = k.g * p.in_bs + (long long)row0 * p.ldi + m;
-    const int cols = mcol > 0 ? 32 : 0;
-    tg_piece_out(slot, reinterpret_cast<__half*>(p.out) + at, p.ldi, nrow, cols, lane);
-    tg_piece_out(slot + kTgPiece, p.lo + at, p.ldi, nrow, cols, lane);
+    tg_piece_out(slot, reinterpret_cast<__half*>(p.out) + k.g * p.in_bs + (long long)row0 * p.ldi + m, p.ldi, nrow,
+                 mcol > 0 ? 32 : 0, lane);
   } else {
     tg_piece_put<kRowsN>(slot, v, lane);
     __syncwarp();
@@ -814,17 +846,17 @@ __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v
   __syncwarp();   // the slot is free for the next input
 }
 
-// The accumulator of the next piece is on its way from TMEM while a piece is
-// stored, and the accumulator buffer is given back before the last one is.
+// The accumulator of the next piece (and its low bits of X) is on its way while
+// a piece is stored, and the accumulator buffer is given back before the last
+// piece is.
 template <int Epi, typename T>
 __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32_t tmem, uint32_t rank, int warp) {
+  constexpr bool kWide = Epi == kTgUpdate || Epi == kTgUpdateOut;
   const int lane = ptx::lane_id();
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t leader_empty0 = ptx::mapa(ptx::smem_u32(&s.acc_empty[0]), 0);
-  const bool reads = Epi == kTgPoly || Epi == kTgUpdate || Epi == kTgUpdateOut || (Epi == kTgStore && p.res != nullptr);
-  constexpr int kSlot = tg_planes<Epi>() * kTgPiece;
-  const uint32_t base = store + (warp - 4) * kSlot * (Epi == kTgStore && !reads ? 1 : 2);
-  int slot = 0;
+  const bool reads = Epi == kTgPoly || kWide || (Epi == kTgStore && p.res != nullptr);
+  const uint32_t base = store + (warp - 4) * kTgPiece * tg_slots<Epi>(p.res != nullptr);
   int acc = 0;
   uint32_t acc_phase = 0;
   TgCursor list;
@@ -833,7 +865,13 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
   while (more) {
     const bool any = k.klen > 0;
     const int m = k.m0 + (int)rank * 128 + quad * 32;
-    if (reads && part * 32 < k.nt) tg_prefetch<Epi, T>(base + slot * kSlot, p, k, part, m, lane);
+    uint32_t slot = base;
+    if (reads) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)   // one group each, empty past the tile
+        if ((part + 2 * c) * 32 < k.nt) tg_prefetch<Epi, T>(base + c * kTgPiece, p, k, part + 2 * c, m, lane);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     float bias[4] = {0.f, 0.f, 0.f, 0.f};
     float alpha = 1.f;
     if (Epi == kTgStore) {
@@ -843,6 +881,13 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
           if (m + 8 * b < p.M) bias[b] = (float)reinterpret_cast<const T*>(p.bias)[m + 8 * b + (lane >> 2)];
     } else if (p.alpha != nullptr) {
       alpha = p.alpha[k.g];
+    }
+    const bool low = kWide && p.lo_in != nullptr && m < p.M;
+    uint4 l0 = make_uint4(0, 0, 0, 0), l1 = l0;
+    if (low && part * 32 < k.nt) {
+      const uint4* at = reinterpret_cast<const uint4*>(p.lo_in + tg_low_at(p, k, part, m, lane));
+      l0 = at[0];
+      l1 = at[1];
     }
     uint32_t r[2][16];
     const uint32_t from = tmem + acc * 256 + ((uint32_t)(quad * 32) << 16);
@@ -855,16 +900,21 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
       }
     }
     more = list.next(next, p, s);
+#pragma unroll 1
     for (int c = part; c * 32 < k.nt; c += 2) {
       const bool again = (c + 2) * 32 < k.nt;
       if (reads) {
-        if (again) {
-          tg_prefetch<Epi, T>(base + (slot ^ 1) * kSlot, p, k, c + 2, m, lane);
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
+        if (c < 2) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (c < 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (c < 6) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
+      }
+      uint32_t v[16], lo[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+      if (low && again) {
+        const uint4* at = reinterpret_cast<const uint4*>(p.lo_in + tg_low_at(p, k, c + 2, m, lane));
+        l0 = at[0];
+        l1 = at[1];
       }
       if (any) {
         ptx::tmem_ld_wait();
@@ -872,8 +922,7 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
       }
-      uint32_t v[16], lo[16];
-      tg_piece_value<Epi, T>(base + slot * kSlot, r, v, lo, p, k, c, m, lane, bias, alpha);
+      tg_piece_value<Epi, T>(slot, r, v, lo, p, k, c, m, lane, bias, alpha);
       if (any && again) {
         tg_tmem_frag(from + (c + 2) * 32, r[0]);
         tg_tmem_frag(from + (c + 2) * 32 + (16u << 16), r[1]);
@@ -883,8 +932,8 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
       }
-      tg_piece_store<Epi, T>(base + slot * kSlot, v, lo, p, k, c, m, lane);
-      if (reads) slot ^= 1;
+      tg_piece_store<Epi, T>(slot, v, lo, p, k, c, m, lane);
+      if (reads) slot += kTgPiece;
     }
     if (any) {
       if (part * 32 >= k.nt && lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
@@ -946,28 +995,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
         tg_set_error(p, s, kDevBounds, false);
         lo = hi = 0;
       }
-      s.start[e] = lo;
-      s.count[e] = hi - lo;
+      s.start()[e] = lo;
+      s.count(p.groups)[e] = hi - lo;
     }
   }
   __syncthreads();
   if (Mode == kTgRaggedN) {
     if (warp == 0) {
+      const int* count = s.count(p.groups);
+      int* tile0 = s.tile0(p.groups);
       int run = 0;
       for (int b = 0; b < p.groups; b += 32) {
         const int e = b + lane;
-        const int mine = e < p.groups ? (s.count[e] + p.nt - 1) / p.nt : 0;
+        const int mine = e < p.groups ? (count[e] + p.nt - 1) / p.nt : 0;
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int up = __shfl_up_sync(0xffffffffu, sum, d);
           if (lane >= d) sum += up;
         }
-        if (e < p.groups) s.tile0[e] = run + sum - mine;
+        if (e < p.groups) tile0[e] = run + sum - mine;
         run += __shfl_sync(0xffffffffu, sum, 31);
       }
       if (lane == 0) {
-        s.tile0[p.groups] = run;
+        tile0[p.groups] = run;
         s.total = run * mt;
       }
     }
