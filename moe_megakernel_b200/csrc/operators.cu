@@ -130,6 +130,21 @@ int launch(TgParams& p, long long tiles, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// An element pass of 256 threads a block (operators.cuh), launched in the same way.
+template <typename P>
+int launch_pass(void (*kernel)(P), dim3 grid, const P& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool operand_ok(const void* p) { return p != nullptr && aligned(p, 16); }
 bool pitch_ok(long long ld, int width) { return ld >= width && ld % 8 == 0 && ld < (1ll << 36); }
@@ -453,15 +468,13 @@ extern "C" int moe_linear_backward(const void* dy, long long lddy, const void* x
     const int chunks = bias_chunks(T);
     ActParams a{dy, lddy, preact, ldz, act ? dz : nullptr, dbias ? partial : nullptr, dbias, T, N,
                 (T + chunks - 1) / chunks, chunks, activation};
-    const dim3 grid((N + kActCols - 1) / kActCols, chunks);
-    if (dtype == MOE_DTYPE_FP16) moe_act_backward_kernel<__half><<<grid, 256, 0, st>>>(a);
-    else moe_act_backward_kernel<bf16><<<grid, 256, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    if (dbias != nullptr) {
-      if (dtype == MOE_DTYPE_FP16) moe_bias_sum_kernel<__half><<<(N + 31) / 32, 256, 0, st>>>(a);
-      else moe_bias_sum_kernel<bf16><<<(N + 31) / 32, 256, 0, st>>>(a);
-      if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    }
+    const bool h = dtype == MOE_DTYPE_FP16;
+    if (int rc = launch_pass(h ? moe_act_backward_kernel<__half> : moe_act_backward_kernel<bf16>,
+                             dim3((N + kActCols - 1) / kActCols, chunks), a, st))
+      return rc;
+    if (dbias != nullptr)
+      if (int rc = launch_pass(h ? moe_bias_sum_kernel<__half> : moe_bias_sum_kernel<bf16>, dim3((N + 31) / 32), a, st))
+        return rc;
   }
   if (dx != nullptr) {
     TgParams p{};
@@ -515,81 +528,100 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
                 L.bsl, (int)std::min<long long>(kOrthoChunks, ((long long)m * n + 4095) / 4096)};
   const bool fp32 = dtype == MOE_DTYPE_FP32;
   const dim3 grid(o.chunks, batch);
-  if (fp32) {
-    moe_ortho_norm_kernel<float><<<grid, 256, 0, st>>>(o);
-    moe_ortho_scale_fp32_kernel<<<grid, 256, 0, st>>>(o);
-  } else {
-    moe_ortho_norm_kernel<bf16><<<grid, 256, 0, st>>>(o);
-    moe_ortho_scale_bf16_kernel<<<grid, 256, 0, st>>>(o);
-  }
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  if (int rc = launch_pass(fp32 ? moe_ortho_norm_kernel<float> : moe_ortho_norm_kernel<bf16>, grid, o, st)) return rc;
+  if (int rc = launch_pass(fp32 ? moe_ortho_scale_fp32_kernel : moe_ortho_scale_bf16_kernel, grid, o, st)) return rc;
 
   const Operand A{ws + L.a, (uint64_t)p0, (uint64_t)p0, (uint64_t)L.lda, (uint64_t)batch, (uint64_t)L.bsa};
   const Operand B{ws + L.b, (uint64_t)p0, (uint64_t)p0, (uint64_t)L.lda, (uint64_t)batch, (uint64_t)L.bsa};
-  for (int i = 0; i < steps; ++i) {
-    const Operand X{ws + L.x[i & 1], (uint64_t)n, (uint64_t)m, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
-    const float a = coeffs[3 * i], b = coeffs[3 * i + 1], c = coeffs[3 * i + 2];
-    const float* alpha = i == 0 ? o.alpha : nullptr;
-    const int mt = (p0 + 255) / 256;
-    const long long tri = (long long)batch * mt * (mt + 1) / 2;
-    TgParams g{};
-    g.err = error_word;
-    g.f16 = 1;
-    g.groups = batch;
+  TgParams base{};
+  base.err = error_word;
+  base.f16 = 1;
+  base.groups = batch;
+  // A = X X^T (X^T X for a tall X), from X in buffer k
+  auto gram = [&](int k, TgParams& g) {
+    const Operand X{ws + L.x[k], (uint64_t)n, (uint64_t)m, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
+    g = base;
     g.M = g.N = p0;
+    g.K = q0;
     g.nt = 256;
+    g.out = ws + L.a;
+    g.ldo = L.lda;
+    g.out_bs = L.bsa;
+    g.factors.cb = as / (xs * xs);
+    g.backwards = 1;   // from the batches that the step before wrote last, which L2 still holds
+    return set_maps(g, X, tall, X, tall);
+  };
+  // B = b A + c A A
+  auto poly = [&](TgParams& g) {
+    g = base;
+    g.M = g.N = g.K = p0;
+    g.nt = 256;
+    g.out = ws + L.b;
+    g.in = reinterpret_cast<const __half*>(ws + L.a);
     g.ldo = g.ldi = L.lda;
     g.out_bs = g.in_bs = L.bsa;
-    // A = X X^T (X^T X for a tall X)
-    TgParams g1 = g;
-    g1.K = q0;
-    g1.out = ws + L.a;
-    g1.alpha = alpha;
-    g1.cb = as / (xs * xs);
-    g1.backwards = 1;   // from the batches that the step before wrote last, which L2 still holds
-    if (!set_maps(g1, X, tall, X, tall)) return MOE_ERR_CUDA;
-    int rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(g1, tri, st)
-                  : launch<kTgSymmetric, false, false, kTgGram, __half>(g1, tri, st);
-    if (rc) return rc;
-    // B = b A + c A A
-    TgParams g2 = g;
-    g2.K = p0;
-    g2.out = ws + L.b;
-    g2.in = reinterpret_cast<const __half*>(ws + L.a);
-    g2.ca = b;
-    g2.cb = c / as;
-    if (!set_maps(g2, A, false, A, false)) return MOE_ERR_CUDA;
-    if ((rc = launch<kTgSymmetric, false, false, kTgPoly, __half>(g2, tri, st))) return rc;
-    // X' = a X + B X: rows of X on the N side, its columns on the M side
-    TgParams g3 = g;
+    return set_maps(g, A, false, A, false);
+  };
+  // X' = a X + B X, from buffer k to the other (last: to the caller); rows of X on the N side, columns on the M side:
+  // wide X'[r, c] = sum_k X[k, c] B[r, k], tall X'[r, c] = sum_k B[c, k] X[r, k] (B symmetric)
+  auto update = [&](int k, bool last, TgParams& g) {
+    const Operand X{ws + L.x[k], (uint64_t)n, (uint64_t)m, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
+    g = base;
+    g.M = n;
+    g.N = m;
+    g.K = p0;
+    g.nt = pick_tile(m, (n + 255) / 256, batch, pairs, false);
+    g.in = reinterpret_cast<const __half*>(ws + L.x[k]);
+    g.lo_out = ws + L.lo;
+    g.lo_bs = L.bsl;
+    g.ldi = L.ldx;
+    g.in_bs = L.bsx;
+    g.out = last ? out : ws + L.x[k ^ 1];
+    g.ldo = last ? ldo : L.ldx;
+    g.out_bs = last ? bso : L.bsx;
+    return tall ? set_maps(g, B, false, X, false) : set_maps(g, X, true, B, false);
+  };
+  const uint8_t* lo_first = fp32 ? ws + L.lo : nullptr;   // a scaled bf16 gradient needs none
+  // the symmetric products: half of the 256 x 256 tiles, stored twice; or, where these would leave most
+  // pairs idle, all tiles of a width that fills them (with the costs of pick_tile)
+  const int mt = (p0 + 255) / 256;
+  const long long tri = (long long)batch * mt * (mt + 1) / 2;
+  const int all_nt = pick_tile(p0, mt, batch, pairs, tall);
+  const long long all = (long long)((p0 + all_nt - 1) / all_nt) * mt * batch;
+  const bool half = (tri + pairs - 1) / pairs * (256 + 256) <= (all + pairs - 1) / pairs * (256 + all_nt);
+  TgParams g1[2], g2, g3[2], g4;
+  if (!gram(0, g1[0]) || !gram(1, g1[1]) || !poly(g2) || !update(0, false, g3[0]) || !update(1, false, g3[1]) ||
+      !update((steps - 1) & 1, true, g4))
+    return MOE_ERR_CUDA;
+  const long long tiles = (long long)((m + g4.nt - 1) / g4.nt) * ((n + 255) / 256) * batch;
+  if (tri >= (1ll << 30) || tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  for (int i = 0; i < steps; ++i) {
     const bool last = i == steps - 1;
-    g3.M = n;
-    g3.N = m;
-    g3.K = p0;
-    g3.nt = pick_tile(m, (n + 255) / 256, batch, pairs, false);
-    g3.in = reinterpret_cast<const __half*>(ws + L.x[i & 1]);
-    g3.lo_in = i == 0 && !fp32 ? nullptr : ws + L.lo;   // a scaled bf16 gradient needs none
-    g3.lo_out = ws + L.lo;
-    g3.lo_bs = L.bsl;
-    g3.ldi = L.ldx;
-    g3.in_bs = L.bsx;
-    g3.alpha = alpha;
+    const float* alpha = i == 0 ? o.alpha : nullptr;
+    TgParams& a = g1[i & 1];
+    a.factors.alpha = alpha;
+    g2.factors = TgFactors{coeffs[3 * i + 1], coeffs[3 * i + 2] / as, nullptr, nullptr};
+    int rc;
+    if (half) {
+      rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(a, tri, st)
+                : launch<kTgSymmetric, false, false, kTgGram, __half>(a, tri, st);
+      if (rc == MOE_OK) rc = launch<kTgSymmetric, false, false, kTgPoly, __half>(g2, tri, st);
+    } else {
+      a.nt = g2.nt = all_nt;
+      rc = tall ? launch<kTgBatched, true, true, kTgGram, __half>(a, all, st)
+                : launch<kTgBatched, false, false, kTgGram, __half>(a, all, st);
+      if (rc == MOE_OK) rc = launch<kTgBatched, false, false, kTgPoly, __half>(g2, all, st);
+    }
+    if (rc) return rc;
+    TgParams& x = last ? g4 : g3[i & 1];
     const float back = last ? 1.f / xs : 1.f;
-    g3.ca = a * back;
-    g3.cb = back / as;
-    g3.out = last ? out : ws + L.x[(i + 1) & 1];
-    g3.ldo = last ? ldo : L.ldx;
-    g3.out_bs = last ? bso : L.bsx;
-    // wide: X'[r, c] = sum_k X[k, c] B[r, k];  tall: X'[r, c] = sum_k B[c, k] X[r, k]  (B symmetric)
-    if (!(tall ? set_maps(g3, B, false, X, false) : set_maps(g3, X, true, B, false))) return MOE_ERR_CUDA;
-    const long long tiles = (long long)((m + g3.nt - 1) / g3.nt) * ((n + 255) / 256) * batch;
-    if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    x.factors = TgFactors{coeffs[3 * i] * back, back / as, alpha, i == 0 ? lo_first : ws + L.lo};
     if (tall)
-      rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(g3, tiles, st)
-                : launch<kTgBatched, false, false, kTgUpdate, __half>(g3, tiles, st);
+      rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(x, tiles, st)
+                : launch<kTgBatched, false, false, kTgUpdate, __half>(x, tiles, st);
     else
-      rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(g3, tiles, st)
-                : launch<kTgBatched, true, false, kTgUpdate, __half>(g3, tiles, st);
+      rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(x, tiles, st)
+                : launch<kTgBatched, true, false, kTgUpdate, __half>(x, tiles, st);
     if (rc) return rc;
   }
   return MOE_OK;

@@ -80,6 +80,8 @@ __device__ __forceinline__ void act_rows(const ActParams& p, int col, int first,
 
 template <typename T>
 __global__ void __launch_bounds__(256) moe_act_backward_kernel(const ActParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tg_after_stream();
   __shared__ float sums[8][kActCols];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int col = blockIdx.x * kActCols + tx * 8;
@@ -110,6 +112,8 @@ __global__ void __launch_bounds__(256) moe_act_backward_kernel(const ActParams p
 // 32 columns a block, the chunks' sums over 8 warps.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_bias_sum_kernel(const ActParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tg_after_stream();
   __shared__ float sums[8][32];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
@@ -184,6 +188,8 @@ __device__ __forceinline__ void ortho_load8(const T* p, float (&v)[8]) {
 // Squares summed in fp64: neither a large fp32 gradient overflows nor a small one vanishes.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_ortho_norm_kernel(const OrthoParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tg_after_stream();
   __shared__ double scratch[8];
   const T* g = reinterpret_cast<const T*>(p.g) + blockIdx.y * p.bsg;
   const bool wide = ortho_wide<T>(p);
@@ -234,6 +240,8 @@ __device__ __forceinline__ double ortho_scale(const OrthoParams& p, double* scra
 }
 
 __global__ void __launch_bounds__(256) moe_ortho_scale_bf16_kernel(const OrthoParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tg_after_stream();
   __shared__ double scratch[8];
   const double scale = ortho_scale(p, scratch);
   const bf16* g = reinterpret_cast<const bf16*>(p.g) + blockIdx.y * p.bsg;
@@ -264,6 +272,8 @@ __global__ void __launch_bounds__(256) moe_ortho_scale_bf16_kernel(const OrthoPa
 
 // fp32: a warp turns 32 x 32 pieces into the update epilogue's order.
 __global__ void __launch_bounds__(256) moe_ortho_scale_fp32_kernel(const OrthoParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tg_after_stream();
   __shared__ double scratch[8];
   __shared__ __align__(128) uint8_t stage[8][kTgPiece];
   const double scale = ortho_scale(p, scratch);

@@ -59,6 +59,13 @@ enum TgEpilogue : int {
 
 enum TgAct : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
+// The Newton-Schulz epilogues' coefficients.
+struct TgFactors {
+  float ca, cb;           // on the stored value and on the accumulator
+  const float* alpha;     // [batches] or null: times the update, squared times the Gram matrix
+  const uint8_t* lo_in;   // the low bits of X, or null
+};
+
 struct TgParams {
   CUtensorMap tm_p;      // K-major: {k, m, batch} box {64, 128}; MN-major: {m, k, batch} box {64, 64}
   CUtensorMap tm_q[4];   // K-major: {k, n, batch} boxes of 128, 64, 32, 16 rows; MN-major: [0] box {64, 64}
@@ -81,11 +88,9 @@ struct TgParams {
   int act;
   // Newton-Schulz
   const __half* in;         // kTgPoly: A; kTgUpdate: X, the fp16 part
-  const uint8_t* lo_in;     // kTgUpdate: X, the 8 bits below it, in pieces (null: none)
-  uint8_t* lo_out;
+  uint8_t* lo_out;          // kTgUpdate: X, the 8 bits below it, in pieces
   long long ldi, in_bs, lo_bs;
-  const float* alpha;       // [batches]: the first step's normalisation, or null
-  float ca, cb;             // coefficients on the stored value and on the accumulator
+  TgFactors factors;
   int backwards;            // batches from the last to the first
 };
 
@@ -96,6 +101,7 @@ struct TgTask {
   int cols;     // valid N rows
   int nt;       // MMA columns (multiple of 32)
   int k0, klen; // reduction range
+  int mirror;   // the tile is also stored transposed (symmetric products, off the diagonal)
 };
 
 struct TgSmem {
@@ -219,6 +225,7 @@ __device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, TgSmem& s)
     k.n0 = r << 8;
     k.cols = min(256, p.N - k.n0);
     k.klen = p.K;
+    k.mirror = k.m0 != k.n0;
   } else {
     const int ntl = (p.N + p.nt - 1) / p.nt;
     k.g = t / (mt * ntl);
@@ -242,28 +249,6 @@ __device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, TgSmem& s)
 __device__ __forceinline__ int tg_ksteps(const TgTask& k, int kb) { return min(4, (k.klen - kb * 64 + 15) >> 4); }
 
 // ---------------------------------------------------------------- list of tiles (warp 3)
-template <int Mode>
-__device__ void tg_schedule(const TgParams& p, TgSmem& s, int first, int step) {
-  int q = 0;
-  uint32_t phase = 0;
-  for (int t = first;; t += step) {
-    TgTask k{};
-    k.g = -1;
-    if (t < s.total) k = tg_decode<Mode>(t, p, s);
-    if (!tg_wait_warp(&s.task_empty[q], phase ^ 1, p, s)) return;
-    if (ptx::lane_id() == 0) {
-      s.task[q] = k;
-      ptx::mbar_arrive(&s.task_full[q]);
-    }
-    __syncwarp();
-    if (k.g < 0) return;
-    if (++q == kTgRing) {
-      q = 0;
-      phase ^= 1;
-    }
-  }
-}
-
 // A warp's place in the list.
 struct TgCursor {
   int q = 0;
@@ -274,13 +259,55 @@ struct TgCursor {
     k = s.task[q];
     __syncwarp();
     if (ptx::lane_id() == 0) ptx::mbar_arrive(&s.task_empty[q]);
+    step();
+    return k.g >= 0;
+  }
+  __device__ __forceinline__ void step() {
     if (++q == kTgRing) {
       q = 0;
       phase ^= 1;
     }
-    return k.g >= 0;
   }
 };
+
+// Where a role stands in the rings of stages, accumulators and tiles; one per
+// warp, carried from product to product where a kernel runs several.
+struct TgState {
+  int stage = 0;
+  uint32_t phase = 0;
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  TgCursor list;
+  __device__ __forceinline__ void next_stage(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void next_acc() {
+    if (++acc == 2) {
+      acc = 0;
+      acc_phase ^= 1;
+    }
+  }
+};
+
+template <int Mode>
+__device__ void tg_schedule(const TgParams& p, TgSmem& s, TgState& at, int first, int end, int step) {
+  for (int t = first;; t += step) {
+    TgTask k{};
+    k.g = -1;
+    if (t < end) k = tg_decode<Mode>(t, p, s);
+    if (!tg_wait_warp(&s.task_empty[at.list.q], at.list.phase ^ 1, p, s)) return;
+    if (ptx::lane_id() == 0) {
+      s.task[at.list.q] = k;
+      ptx::mbar_arrive(&s.task_full[at.list.q]);
+    }
+    __syncwarp();
+    at.list.step();
+    if (k.g < 0) return;
+  }
+}
 
 // ---------------------------------------------------------------- loads
 __device__ __forceinline__ void tg_load3(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
@@ -333,46 +360,38 @@ __device__ __forceinline__ bool tg_has_tail(const TgTask& k, int kb) {
 }
 
 template <int Mode, bool PMn, bool QMn>
-__device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t rank) {
-  int stage = 0;
-  uint32_t phase = 0;
+__device__ void tg_producer(const TgParams& p, TgSmem& s, TgState& at, uint32_t tiles, uint32_t rank) {
   bool ok = true;
-  TgCursor list;
   TgTask k;
-  while (ok && list.next(k, p, s)) {
+  while (ok && at.list.next(k, p, s)) {
     const int nk = (k.klen + 63) >> 6;
     const uint32_t tx = tg_stage_tx<QMn>(k);
     const int pbatch = Mode == kTgRaggedK ? 0 : k.g;
     const int qbatch = Mode == kTgRaggedK || Mode == kTgRaggedN ? 0 : k.g;
     for (int kb = 0; kb < nk; ++kb) {
-      if (!tg_wait_warp(&s.empty[stage], phase ^ 1, p, s)) {
+      if (!tg_wait_warp(&s.empty[at.stage], at.phase ^ 1, p, s)) {
         ok = false;
         break;
       }
-      const uint32_t dst = tiles + stage * p.stage_bytes;
+      const uint32_t dst = tiles + at.stage * p.stage_bytes;
       const bool tail = tg_has_tail<Mode>(k, kb);
       // both CTAs' bytes on the leader's barrier; a tail block's on each CTA's own
-      const uint32_t bar = tail ? ptx::mapa(ptx::smem_u32(&s.tail[stage]), rank)
-                                : ptx::mapa(ptx::smem_u32(&s.full[stage]), 0);
+      const uint32_t bar = tail ? ptx::mapa(ptx::smem_u32(&s.tail[at.stage]), rank)
+                                : ptx::mapa(ptx::smem_u32(&s.full[at.stage]), 0);
       if (tg_elect()) {
-        if (tail) ptx::mbar_arrive_expect_tx(&s.tail[stage], tx);
-        else if (rank == 0) ptx::mbar_arrive_expect_tx(&s.full[stage], 2 * tx);
+        if (tail) ptx::mbar_arrive_expect_tx(&s.tail[at.stage], tx);
+        else if (rank == 0) ptx::mbar_arrive_expect_tx(&s.full[at.stage], 2 * tx);
         tg_load_stage<PMn, QMn>(dst, p, k, k.k0 + kb * 64, rank, bar, pbatch, qbatch);
       }
       __syncwarp();
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
+      at.next_stage(p.stages);
     }
   }
   // the commits that free the stages have arrived before this CTA's barriers go away
+  TgState drain = at;
   for (int i = 0; ok && i < p.stages; ++i) {
-    ok = tg_wait_warp(&s.empty[stage], phase ^ 1, p, s);
-    if (++stage == p.stages) {
-      stage = 0;
-      phase ^= 1;
-    }
+    ok = tg_wait_warp(&s.empty[drain.stage], drain.phase ^ 1, p, s);
+    drain.next_stage(p.stages);
   }
   if (!ok) {   // given up: let the copies in flight land before the shared memory goes away
     for (int i = 0; i < 5000; ++i) __nanosleep(1000);
@@ -385,13 +404,12 @@ __device__ void tg_producer(const TgParams& p, TgSmem& s, uint32_t tiles, uint32
 // last step are overwritten with zeros in both operands (zeros in one alone
 // would still meet an infinity or NaN of another group in the other).
 template <int Mode>
-__device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint32_t rank) {
+__device__ void tg_tail_warp(const TgParams& p, TgSmem& s, TgState& at, uint8_t* tiles, uint32_t rank) {
   const int lane = ptx::lane_id();
   int stage = 0;
   uint32_t used = 0;   // parity of each stage's tail barrier
-  TgCursor list;
   TgTask k;
-  while (list.next(k, p, s)) {
+  while (at.list.next(k, p, s)) {
     const int nk = (k.klen + 63) >> 6;
     if (nk == 0) continue;
     const int last = (stage + nk - 1) % p.stages;
@@ -399,10 +417,10 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint3
       if (!tg_wait_warp(&s.tail[last], (used >> last) & 1, p, s)) return;
       const int r0 = k.klen & 63, r1 = (r0 + 15) & ~15;
       const int boxes = 2 + (((k.nt >> 1) + 63) >> 6);
-      uint8_t* at = tiles + (size_t)last * p.stage_bytes;
+      uint8_t* rows = tiles + (size_t)last * p.stage_bytes;
       for (int b = 0; b < boxes; ++b)
         for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
-          *reinterpret_cast<uint4*>(at + b * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(rows + b * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
       ptx::fence_proxy_async_shared();
       __syncwarp();
       if (rank != 0) {
@@ -424,7 +442,7 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, uint8_t* tiles, uint3
 // cycles to issue, more than its share of the tensor core's time (64 at 256
 // columns and two CTAs' operands).
 template <int Mode, bool PMn, bool QMn>
-__device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tmem) {
+__device__ void tg_mma(const TgParams& p, TgSmem& s, TgState& at, uint32_t tiles, uint32_t tmem) {
   const uint32_t fmt = p.f16 ? 0u : 1u;
   const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((PMn ? 1u : 0u) << 15) | ((QMn ? 1u : 0u) << 16) |
                           ((256u >> 4) << 24);
@@ -432,42 +450,31 @@ __device__ void tg_mma(const TgParams& p, TgSmem& s, uint32_t tiles, uint32_t tm
   const uint64_t qdesc = QMn ? ptx::smem_desc_sw128(tiles + kTgABytes, 8192, 1024)
                              : ptx::smem_desc_sw128(tiles + kTgABytes, 16, 1024);
   constexpr uint64_t pstep = (PMn ? 2048 : 32) >> 4, qstep = (QMn ? 2048 : 32) >> 4;   // 16 k further
-  int stage = 0;
-  uint32_t phase = 0;
-  int acc = 0;
-  uint32_t acc_phase = 0;
-  TgCursor list;
   TgTask k;
-  while (list.next(k, p, s)) {
+  while (at.list.next(k, p, s)) {
     const int nk = (k.klen + 63) >> 6;
     if (nk == 0) continue;
-    if (!tg_wait_warp(&s.acc_empty[acc], acc_phase ^ 1, p, s)) return;
+    if (!tg_wait_warp(&s.acc_empty[at.acc], at.acc_phase ^ 1, p, s)) return;
     ptx::tc_fence_after();
-    const uint32_t d = tmem + acc * 256;
+    const uint32_t d = tmem + at.acc * 256;
     const uint32_t idesc = idesc0 | ((uint32_t)(k.nt >> 3) << 17);
     for (int kb = 0; kb < nk; ++kb) {
-      if (!tg_wait_warp(&s.full[stage], phase, p, s)) return;
+      if (!tg_wait_warp(&s.full[at.stage], at.phase, p, s)) return;
       ptx::tc_fence_after();
-      const uint64_t off = (uint64_t)(uint32_t)(stage * p.stage_bytes) >> 4;
+      const uint64_t off = (uint64_t)(uint32_t)(at.stage * p.stage_bytes) >> 4;
       const int steps = Mode == kTgRaggedK ? tg_ksteps(k, kb) : 4;
       if (tg_elect()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           if (Mode != kTgRaggedK || kk < steps)
             ptx::mma_bf16_pair(d, pdesc + off + kk * pstep, qdesc + off + kk * qstep, idesc, (kb | kk) != 0 ? 1u : 0u);
-        ptx::mma_commit_pair_multicast(&s.empty[stage], 0x3);
-        if (kb == nk - 1) ptx::mma_commit_pair_multicast(&s.acc_full[acc], 0x3);
+        ptx::mma_commit_pair_multicast(&s.empty[at.stage], 0x3);
+        if (kb == nk - 1) ptx::mma_commit_pair_multicast(&s.acc_full[at.acc], 0x3);
       }
       __syncwarp();
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
+      at.next_stage(p.stages);
     }
-    if (++acc == 2) {
-      acc = 0;
-      acc_phase ^= 1;
-    }
+    at.next_acc();
   }
 }
 
@@ -668,7 +675,7 @@ __device__ __forceinline__ void tg_pack(const uint32_t (&r)[2][16], uint32_t (&v
                                      __uint_as_float(r[b >> 1][4 * i + 2 * (b & 1) + 1]));
 }
 
-// Pieces a warp keeps in shared memory: all four of its share of a tile when the
+// Pieces a warp keeps in shared memory: all of its share of a tile when the
 // epilogue reads, so that a tile's whole input is on its way before its MMAs end
 // (with two, the wait for each third and fourth piece took longer than the piece).
 template <int Epi>
@@ -722,7 +729,7 @@ __device__ __forceinline__ long long tg_low_at(const TgParams& p, const TgTask& 
 template <int Epi, typename T>
 __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][16], uint32_t (&v)[16],
                                                uint32_t (&lo)[8], const TgParams& p, const TgTask& k, int c, int m,
-                                               int lane, const float (&bias)[4], float alpha) {
+                                               int lane, const float (&bias)[4], float ca, float cb) {
   if (Epi == kTgStore) {
     uint32_t res[16];
     if (p.res != nullptr) tg_piece_get<kRowsN>(slot, res, lane);
@@ -757,7 +764,6 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
     }
     tg_pack<T>(r, v);
   } else if (Epi == kTgGram || Epi == kTgPoly) {
-    const float cb = p.cb * alpha * alpha;
     if (Epi == kTgPoly) tg_piece_get<kRowsM>(slot, v, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -767,14 +773,13 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
         float x = cb * __uint_as_float(e[0]), y = cb * __uint_as_float(e[1]);
         if (Epi == kTgPoly) {
           const float2 f = TgPair<__half>::unpack(v[4 * i + b]);
-          x += p.ca * f.x;
-          y += p.ca * f.y;
+          x += ca * f.x;
+          y += ca * f.y;
         }
         v[4 * i + b] = TgPair<__half>::pack(x, y);
       }
   } else {
     tg_piece_get<kRowsN>(slot, v, lane);
-    const float ca = alpha * p.ca, cb = alpha * p.cb;
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {   // two 8 x 8 blocks: four values, one word of low bits
       int q[4];
@@ -817,7 +822,7 @@ __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v
     tg_piece_put<kRowsM>(slot, v, lane);
     __syncwarp();
     tg_piece_out(slot, out + (long long)m * p.ldo + row0, p.ldo, mcol, 32, lane);
-    if (k.m0 != k.n0) {
+    if (k.mirror) {
       __syncwarp();
       tg_piece_put<kRowsN>(slot, v, lane);
       __syncwarp();
@@ -850,26 +855,25 @@ __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v
 // a piece is stored, and the accumulator buffer is given back before the last
 // piece is.
 template <int Epi, typename T>
-__device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32_t tmem, uint32_t rank, int warp) {
+__device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, TgState& at, uint32_t store, uint32_t tmem,
+                            uint32_t rank, int warp) {
   constexpr bool kWide = Epi == kTgUpdate || Epi == kTgUpdateOut;
+  constexpr int kParts = kTgEpiWarps / 4;   // warps that share a quarter of the lanes, every kParts-th piece each
   const int lane = ptx::lane_id();
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t leader_empty0 = ptx::mapa(ptx::smem_u32(&s.acc_empty[0]), 0);
   const bool reads = Epi == kTgPoly || kWide || (Epi == kTgStore && p.res != nullptr);
   const uint32_t base = store + (warp - 4) * kTgPiece * tg_slots<Epi>(p.res != nullptr);
-  int acc = 0;
-  uint32_t acc_phase = 0;
-  TgCursor list;
   TgTask k, next;
-  bool more = list.next(k, p, s);
+  bool more = at.list.next(k, p, s);
   while (more) {
     const bool any = k.klen > 0;
     const int m = k.m0 + (int)rank * 128 + quad * 32;
     uint32_t slot = base;
     if (reads) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)   // one group each, empty past the tile
-        if ((part + 2 * c) * 32 < k.nt) tg_prefetch<Epi, T>(base + c * kTgPiece, p, k, part + 2 * c, m, lane);
+      for (int c = 0; c < 8 / kParts; ++c)   // one group each, empty past the tile
+        if ((part + kParts * c) * 32 < k.nt) tg_prefetch<Epi, T>(base + c * kTgPiece, p, k, part + kParts * c, m, lane);
         else asm volatile("cp.async.commit_group;" ::: "memory");
     }
     float bias[4] = {0.f, 0.f, 0.f, 0.f};
@@ -879,42 +883,45 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
 #pragma unroll
         for (int b = 0; b < 4; ++b)
           if (m + 8 * b < p.M) bias[b] = (float)reinterpret_cast<const T*>(p.bias)[m + 8 * b + (lane >> 2)];
-    } else if (p.alpha != nullptr) {
-      alpha = p.alpha[k.g];
+    } else if (f.alpha != nullptr) {
+      alpha = f.alpha[k.g];
     }
-    const bool low = kWide && p.lo_in != nullptr && m < p.M;
+    const float ca = kWide ? f.ca * alpha : f.ca, cb = kWide ? f.cb * alpha : f.cb * alpha * alpha;
+    const bool low = kWide && f.lo_in != nullptr && m < p.M;
     uint4 l0 = make_uint4(0, 0, 0, 0), l1 = l0;
     if (low && part * 32 < k.nt) {
-      const uint4* at = reinterpret_cast<const uint4*>(p.lo_in + tg_low_at(p, k, part, m, lane));
-      l0 = at[0];
-      l1 = at[1];
+      const uint4* from = reinterpret_cast<const uint4*>(f.lo_in + tg_low_at(p, k, part, m, lane));
+      l0 = __ldcg(from);
+      l1 = __ldcg(from + 1);
     }
     uint32_t r[2][16];
-    const uint32_t from = tmem + acc * 256 + ((uint32_t)(quad * 32) << 16);
+    const uint32_t from = tmem + at.acc * 256 + ((uint32_t)(quad * 32) << 16);
     if (any) {
-      if (!tg_wait_warp(&s.acc_full[acc], acc_phase, p, s)) break;
+      if (!tg_wait_warp(&s.acc_full[at.acc], at.acc_phase, p, s)) break;
       ptx::tc_fence_after();
       if (part * 32 < k.nt) {
         tg_tmem_frag(from + part * 32, r[0]);
         tg_tmem_frag(from + part * 32 + (16u << 16), r[1]);
       }
     }
-    more = list.next(next, p, s);
+    more = at.list.next(next, p, s);
 #pragma unroll 1
-    for (int c = part; c * 32 < k.nt; c += 2) {
-      const bool again = (c + 2) * 32 < k.nt;
+    for (int c = part; c * 32 < k.nt; c += kParts) {
+      const bool again = (c + kParts) * 32 < k.nt;
       if (reads) {
-        if (c < 2) asm volatile("cp.async.wait_group 3;" ::: "memory");
-        else if (c < 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else if (c < 6) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        switch (8 / kParts - 1 - c / kParts) {   // groups that may still be under way
+          case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+          case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+          case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+          default: asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
         __syncwarp();
       }
       uint32_t v[16], lo[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
       if (low && again) {
-        const uint4* at = reinterpret_cast<const uint4*>(p.lo_in + tg_low_at(p, k, c + 2, m, lane));
-        l0 = at[0];
-        l1 = at[1];
+        const uint4* low_from = reinterpret_cast<const uint4*>(f.lo_in + tg_low_at(p, k, c + kParts, m, lane));
+        l0 = __ldcg(low_from);
+        l1 = __ldcg(low_from + 1);
       }
       if (any) {
         ptx::tmem_ld_wait();
@@ -922,25 +929,22 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
       }
-      tg_piece_value<Epi, T>(slot, r, v, lo, p, k, c, m, lane, bias, alpha);
+      tg_piece_value<Epi, T>(slot, r, v, lo, p, k, c, m, lane, bias, ca, cb);
       if (any && again) {
-        tg_tmem_frag(from + (c + 2) * 32, r[0]);
-        tg_tmem_frag(from + (c + 2) * 32 + (16u << 16), r[1]);
+        tg_tmem_frag(from + (c + kParts) * 32, r[0]);
+        tg_tmem_frag(from + (c + kParts) * 32 + (16u << 16), r[1]);
       }
       if (any && !again) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
+        if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + at.acc * 8);
       }
       tg_piece_store<Epi, T>(slot, v, lo, p, k, c, m, lane);
       if (reads) slot += kTgPiece;
     }
     if (any) {
-      if (part * 32 >= k.nt && lane == 0) ptx::mbar_arrive_peer(leader_empty0 + acc * 8);
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
+      if (part * 32 >= k.nt && lane == 0) ptx::mbar_arrive_peer(leader_empty0 + at.acc * 8);
+      at.next_acc();
     }
     k = next;
   }
@@ -948,18 +952,14 @@ __device__ void tg_epilogue(const TgParams& p, TgSmem& s, uint32_t store, uint32
 }
 
 // ---------------------------------------------------------------- kernel
-template <int Mode, bool PMn, bool QMn, int Epi, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
-    moe_tile_gemm_kernel(const __grid_constant__ TgParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TgSmem& s = *reinterpret_cast<TgSmem*>(tiles + (size_t)p.stages * p.stage_bytes + p.epi_bytes);
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();
+// The stream's earlier work is done and visible (programmatic stream serialisation).
+__device__ __forceinline__ void tg_after_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Barriers and TMEM; the caller synchronises the cluster afterwards.
+template <bool RaggedK>
+__device__ __forceinline__ void tg_setup(TgSmem& s, int stages, uint32_t rank) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       ptx::mbar_init(&s.full[i], 1);
       ptx::mbar_init(&s.empty[i], 1);
       ptx::mbar_init(&s.tail[i], 1);
@@ -972,22 +972,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
     for (int i = 0; i < kTgRing; ++i) {
       ptx::mbar_init(&s.task_full[i], 1);
       // readers: the producer, the leader's MMA warp, the tail warp of a ragged reduction, the epilogue
-      ptx::mbar_init(&s.task_empty[i], 1 + (rank == 0 ? 1 : 0) + (Mode == kTgRaggedK ? 1 : 0) + kTgEpiWarps);
+      ptx::mbar_init(&s.task_empty[i], 1 + (rank == 0 ? 1 : 0) + (RaggedK ? 1 : 0) + kTgEpiWarps);
     }
     s.abort = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&p.tm_p);
-    for (int i = 0; i < (QMn ? 1 : 4); ++i) ptx::prefetch_tmap(&p.tm_q[i]);
   }
-  if (warp == 3) {
+  if ((threadIdx.x >> 5) == 3) {
     ptx::tmem_alloc_pair(&s.tmem_base, kTmemCols);
     ptx::tmem_relinquish_pair();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the stream's earlier work is done and visible
+}
 
+// One product, all roles: tiles first, first + step, ... below end.
+template <int Mode, bool PMn, bool QMn, int Epi, typename T>
+__device__ __forceinline__ void tg_product(const TgParams& p, const TgFactors& f, TgSmem& s, TgState& at, uint8_t* tiles,
+                                           uint32_t tmem, uint32_t rank, int warp, int first, int end, int step) {
+  const uint32_t base = ptx::smem_u32(tiles);
+  // the roles that touch global memory; the others set out under the end of the previous kernel
+  if (warp == 0 || warp >= 4) tg_after_stream();
+  if (warp == 0) {
+    tg_producer<Mode, PMn, QMn>(p, s, at, base, rank);
+  } else if (warp == 1) {
+    if (rank == 0) tg_mma<Mode, PMn, QMn>(p, s, at, base, tmem);
+  } else if (warp == 2) {
+    if (Mode == kTgRaggedK) tg_tail_warp<Mode>(p, s, at, tiles, rank);
+  } else if (warp == 3) {
+    tg_schedule<Mode>(p, s, at, first, end, step);
+  } else {
+    tg_epilogue<Epi, T>(p, f, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
+  }
+  __syncwarp();
+}
+
+template <int Mode, bool PMn, bool QMn, int Epi, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
+    moe_tile_gemm_kernel(const __grid_constant__ TgParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TgSmem& s = *reinterpret_cast<TgSmem*>(tiles + (size_t)p.stages * p.stage_bytes + p.epi_bytes);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+
+  tg_setup<Mode == kTgRaggedK>(s, p.stages, rank);
+  if (threadIdx.x == 32) {
+    ptx::prefetch_tmap(&p.tm_p);
+    for (int i = 0; i < (QMn ? 1 : 4); ++i) ptx::prefetch_tmap(&p.tm_q[i]);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int mt = (p.M + 255) >> 8;
   if (Mode == kTgRaggedN || Mode == kTgRaggedK) {
+    tg_after_stream();
     const int rows = Mode == kTgRaggedN ? p.N : p.K;
     for (int e = threadIdx.x; e < p.groups; e += kTgThreads) {
       int lo = p.offsets ? p.offsets[e] : 0, hi = p.offsets ? p.offsets[e + 1] : rows;
@@ -1030,20 +1065,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
   ptx::cluster_sync();   // both CTAs' barriers exist before any remote arrive
   ptx::tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
-
-  if (warp == 0) {
-    tg_producer<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), rank);
-  } else if (warp == 1) {
-    if (rank == 0) tg_mma<Mode, PMn, QMn>(p, s, ptx::smem_u32(tiles), tmem);
-  } else if (warp == 2) {
-    if (Mode == kTgRaggedK) tg_tail_warp<Mode>(p, s, tiles, rank);
-  } else if (warp == 3) {
-    tg_schedule<Mode>(p, s, first, step);
-  } else if (warp >= 4) {
-    tg_epilogue<Epi, T>(p, s, ptx::smem_u32(tiles) + p.stages * p.stage_bytes, tmem, rank, warp);
-  }
-  __syncwarp();
+  TgState at;
+  tg_product<Mode, PMn, QMn, Epi, T>(p, p.factors, s, at, tiles, tmem, rank, warp, blockIdx.x >> 1, s.total,
+                                     gridDim.x >> 1);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();   // no peer still arrives on this CTA's barriers or reads its tiles
