@@ -65,6 +65,21 @@ bool set_maps(TgParams& p, const Operand& P, bool p_mn, const Operand& Q, bool q
   return ok;
 }
 
+// The output of a product, written piece by piece: 32 x 32 entries, 64-byte rows swizzled as the epilogue lays them.
+bool set_out(TgParams& p, void* out, uint64_t cols, uint64_t rows, uint64_t pitch, uint64_t batch, uint64_t bs) {
+  EncodeFn enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {cols, rows, batch};
+  const cuuint64_t strides[2] = {pitch * 2, (batch > 1 ? bs : pitch) * 2};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  p.out = out;
+  p.ldo = (long long)pitch;
+  p.out_bs = (long long)bs;
+  return enc(&p.tm_out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, out, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDevices = 64;
 
 int current_device(int* num_sms) {
@@ -280,8 +295,6 @@ int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int r
   p.K = K;
   p.groups = groups;
   p.f16 = dtype == MOE_DTYPE_FP16;
-  p.out = y;
-  p.ldo = ldy;
   const int mt = (N + 255) / 256;
   long long tiles = 0;
   if (p.offsets == nullptr) {
@@ -297,13 +310,15 @@ int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int r
   if (p.offsets == nullptr && rows <= kFewMaxRows) {
     if (sms < 0) return MOE_ERR_UNSUPPORTED_DEVICE;
     const FewCut cut = few_cut(rows, N, K, sms);
+    p.out = y;
+    p.ldo = ldy;
     if (cut.us < pairs_us(tiles, p.nt, K, std::max(1, sms / 2))) {
       if (dtype == MOE_DTYPE_FP16)
         return transpose ? launch_few<false, __half>(p, cut, P, Q, st) : launch_few<true, __half>(p, cut, P, Q, st);
       return transpose ? launch_few<false, bf16>(p, cut, P, Q, st) : launch_few<true, bf16>(p, cut, P, Q, st);
     }
   }
-  if (!set_maps(p, P, !transpose, Q, false)) return MOE_ERR_CUDA;
+  if (!set_maps(p, P, !transpose, Q, false) || !set_out(p, y, N, rows, ldy, 1, 0)) return MOE_ERR_CUDA;
   return transpose ? launch_rows<false>(p, dtype, tiles, st) : launch_rows<true>(p, dtype, tiles, st);
 }
 
@@ -317,16 +332,13 @@ int weight_gradient(TgParams& p, const void* x, long long ldx, const void* dy, l
   p.K = rows;
   p.groups = groups;
   p.f16 = dtype == MOE_DTYPE_FP16;
-  p.out = dW;
-  p.ldo = N;
-  p.out_bs = (long long)K * N;
   const int mt = (N + 255) / 256;
   p.nt = pick_tile(K, mt, groups, std::max(1, sms / 2), true);
   const long long tiles = (long long)((K + p.nt - 1) / p.nt) * mt * groups;
   if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const Operand P{dy, (uint64_t)N, (uint64_t)rows, (uint64_t)lddy, 1, 0};
   const Operand Q{x, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 1, 0};
-  if (!set_maps(p, P, true, Q, true)) return MOE_ERR_CUDA;
+  if (!set_maps(p, P, true, Q, true) || !set_out(p, dW, N, K, N, groups, (uint64_t)K * N)) return MOE_ERR_CUDA;
   return launch_wgrad(p, dtype, tiles, st);
 }
 
@@ -544,23 +556,19 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g.M = g.N = p0;
     g.K = q0;
     g.nt = 256;
-    g.out = ws + L.a;
-    g.ldo = L.lda;
-    g.out_bs = L.bsa;
     g.factors.cb = as / (xs * xs);
     g.backwards = 1;   // from the batches that the step before wrote last, which L2 still holds
-    return set_maps(g, X, tall, X, tall);
+    return set_maps(g, X, tall, X, tall) && set_out(g, ws + L.a, p0, p0, L.lda, batch, L.bsa);
   };
   // B = b A + c A A
   auto poly = [&](TgParams& g) {
     g = base;
     g.M = g.N = g.K = p0;
     g.nt = 256;
-    g.out = ws + L.b;
     g.in = reinterpret_cast<const __half*>(ws + L.a);
-    g.ldo = g.ldi = L.lda;
-    g.out_bs = g.in_bs = L.bsa;
-    return set_maps(g, A, false, A, false);
+    g.ldi = L.lda;
+    g.in_bs = L.bsa;
+    return set_maps(g, A, false, A, false) && set_out(g, ws + L.b, p0, p0, L.lda, batch, L.bsa);
   };
   // X' = a X + B X, from buffer k to the other (last: to the caller); rows of X on the N side, columns on the M side:
   // wide X'[r, c] = sum_k X[k, c] B[r, k], tall X'[r, c] = sum_k B[c, k] X[r, k] (B symmetric)
@@ -576,9 +584,13 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g.lo_bs = L.bsl;
     g.ldi = L.ldx;
     g.in_bs = L.bsx;
-    g.out = last ? out : ws + L.x[k ^ 1];
-    g.ldo = last ? ldo : L.ldx;
-    g.out_bs = last ? bso : L.bsx;
+    if (last) {   // any alignment: no TMA store
+      g.out = out;
+      g.ldo = ldo;
+      g.out_bs = bso;
+    } else if (!set_out(g, ws + L.x[k ^ 1], n, m, L.ldx, batch, L.bsx)) {
+      return false;
+    }
     return tall ? set_maps(g, B, false, X, false) : set_maps(g, X, true, B, false);
   };
   const uint8_t* lo_first = fp32 ? ws + L.lo : nullptr;   // a scaled bf16 gradient needs none

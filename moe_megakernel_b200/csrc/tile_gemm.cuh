@@ -69,6 +69,7 @@ struct TgFactors {
 struct TgParams {
   CUtensorMap tm_p;      // K-major: {k, m, batch} box {64, 128}; MN-major: {m, k, batch} box {64, 64}
   CUtensorMap tm_q[4];   // K-major: {k, n, batch} boxes of 128, 64, 32, 16 rows; MN-major: [0] box {64, 64}
+  CUtensorMap tm_out;    // {m, n, batch} box {32, 32}: one piece of the epilogue (not kTgUpdateOut)
   int M, N, K;           // extents (N: rows of Q in a ragged-N product; K: rows in a ragged-K one)
   int groups;            // groups or batches
   int nt;                // largest N tile: 32, 64, 128 or 256
@@ -655,6 +656,23 @@ __device__ __forceinline__ void tg_piece_in(uint32_t piece, const void* g, long 
     if (row < rows && c * 8 < cols) ptx::cp_async_16(piece + tg_piece_at(row, c), at + i * 8 * ld);
   }
 }
+// A piece as one TMA store (its place order is the 64-byte swizzle), clipped at
+// the tensor's ends. The piece's shared memory is in use until tg_bulk_read.
+__device__ __forceinline__ void tg_piece_bulk(uint32_t piece, const CUtensorMap* m, int c0, int c1, int c2, int lane) {
+  ptx::fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(piece), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    ptx::bulk_commit();
+  }
+}
+__device__ __forceinline__ void tg_bulk_read(int lane) {
+  if (lane == 0) ptx::bulk_wait_read_all();
+  __syncwarp();
+}
 // The same for rows of any alignment and length.
 __device__ __forceinline__ void tg_piece_out_any(uint32_t piece, uint16_t* g, long long ld, int rows, int cols, int lane) {
   if (lane >= cols) return;
@@ -733,18 +751,20 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
   if (Epi == kTgStore) {
     uint32_t res[16];
     if (p.res != nullptr) tg_piece_get<kRowsN>(slot, res, lane);
+    if (p.bias != nullptr) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+      for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
-        e[0] = __float_as_uint(__uint_as_float(e[0]) + bias[b]);
-        e[1] = __float_as_uint(__uint_as_float(e[1]) + bias[b]);
-      }
+        for (int i = 0; i < 4; ++i) {
+          uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
+          e[0] = __float_as_uint(__uint_as_float(e[0]) + bias[b]);
+          e[1] = __float_as_uint(__uint_as_float(e[1]) + bias[b]);
+        }
+    }
     if (p.z != nullptr) {
       const int row0 = k.n0 + c * 32;
       tg_pack<T>(r, v);
-      __syncwarp();
+      tg_bulk_read(lane);
       tg_piece_put<kRowsN>(slot, v, lane);
       __syncwarp();
       tg_piece_out(slot, reinterpret_cast<T*>(p.z) + (long long)row0 * p.ldz + m, p.ldz, k.cols - c * 32, p.M - m,
@@ -805,56 +825,52 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
 }
 
 // Second half: through `slot` to the output.
-template <int Epi, typename T>
+template <int Mode, int Epi, typename T>
 __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v)[16], const uint32_t (&lo)[8],
                                                const TgParams& p, const TgTask& k, int c, int m, int lane) {
   const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
-  __syncwarp();
-  if (Epi == kTgStore) {
-    tg_piece_put<kRowsN>(slot, v, lane);
-    __syncwarp();
-    tg_piece_out(slot, reinterpret_cast<T*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol,
-                 lane);
-  } else if (Epi == kTgGram || Epi == kTgPoly) {
-    // A = X X^T and B = b A + c A A are symmetric: the piece goes out as it lies (row m, whose pitch
-    // is padded to 64, so whole pieces fit) and, off the diagonal tiles, transposed to the mirrored place
-    __half* out = reinterpret_cast<__half*>(p.out) + k.g * p.out_bs;
+  if (Epi == kTgUpdate && mcol > 0 && nrow > 0) {
+    uint4* at = reinterpret_cast<uint4*>(p.lo_out + tg_low_at(p, k, c, m, lane));
+    at[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    at[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+  }
+  tg_bulk_read(lane);   // the slot's last piece has been read (and every lane is done with its input)
+  if (Epi == kTgGram || Epi == kTgPoly) {
+    // A = X X^T and B = b A + c A A are symmetric: the piece goes out as it lies (rows m) and, off the
+    // diagonal tiles, transposed to the mirrored place
+    if (mcol <= 0) return;
     tg_piece_put<kRowsM>(slot, v, lane);
-    __syncwarp();
-    tg_piece_out(slot, out + (long long)m * p.ldo + row0, p.ldo, mcol, 32, lane);
+    tg_piece_bulk(slot, &p.tm_out, row0, m, k.g, lane);
     if (k.mirror) {
-      __syncwarp();
+      tg_bulk_read(lane);
       tg_piece_put<kRowsN>(slot, v, lane);
-      __syncwarp();
-      tg_piece_out(slot, out + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol > 0 ? 32 : 0, lane);
+      tg_piece_bulk(slot, &p.tm_out, m, row0, k.g, lane);
     }
-  } else if (Epi == kTgUpdate) {
-    if (mcol > 0 && nrow > 0) {
-      uint4* at = reinterpret_cast<uint4*>(p.lo_out + tg_low_at(p, k, c, m, lane));
-      at[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      at[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-    }
-    tg_piece_put<kRowsN>(slot, v, lane);
-    __syncwarp();
-    // whole pieces: the pitch is padded to 64
-    tg_piece_out(slot, reinterpret_cast<__half*>(p.out) + k.g * p.in_bs + (long long)row0 * p.ldi + m, p.ldi, nrow,
-                 mcol > 0 ? 32 : 0, lane);
-  } else {
-    tg_piece_put<kRowsN>(slot, v, lane);
+    return;
+  }
+  if (mcol <= 0 || nrow <= 0) return;
+  tg_piece_put<kRowsN>(slot, v, lane);
+  if (Epi == kTgUpdateOut) {
     __syncwarp();
     bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m;
     if (p.ldo % 8 == 0 && p.M % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0)
       tg_piece_out(slot, o, p.ldo, nrow, mcol, lane);
     else
       tg_piece_out_any(slot, reinterpret_cast<uint16_t*>(o), p.ldo, min(nrow, 32), mcol, lane);
+    __syncwarp();
+  } else if (Mode == kTgRaggedN && nrow < 32 && row0 + nrow != p.N) {   // the group ends inside the piece
+    __syncwarp();
+    tg_piece_out(slot, reinterpret_cast<T*>(p.out) + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol, lane);
+    __syncwarp();
+  } else {
+    tg_piece_bulk(slot, &p.tm_out, m, row0, Mode == kTgRaggedN ? 0 : k.g, lane);
   }
-  __syncwarp();   // the slot is free for the next input
 }
 
 // The accumulator of the next piece (and its low bits of X) is on its way while
 // a piece is stored, and the accumulator buffer is given back before the last
 // piece is.
-template <int Epi, typename T>
+template <int Mode, int Epi, typename T>
 __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, TgState& at, uint32_t store, uint32_t tmem,
                             uint32_t rank, int warp) {
   constexpr bool kWide = Epi == kTgUpdate || Epi == kTgUpdateOut;
@@ -871,6 +887,7 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
     const int m = k.m0 + (int)rank * 128 + quad * 32;
     uint32_t slot = base;
     if (reads) {
+      tg_bulk_read(lane);
 #pragma unroll
       for (int c = 0; c < 8 / kParts; ++c)   // one group each, empty past the tile
         if ((part + kParts * c) * 32 < k.nt) tg_prefetch<Epi, T>(base + c * kTgPiece, p, k, part + kParts * c, m, lane);
@@ -939,7 +956,7 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + at.acc * 8);
       }
-      tg_piece_store<Epi, T>(slot, v, lo, p, k, c, m, lane);
+      tg_piece_store<Mode, Epi, T>(slot, v, lo, p, k, c, m, lane);
       if (reads) slot += kTgPiece;
     }
     if (any) {
@@ -949,6 +966,8 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
     k = next;
   }
   ptx::cp_async_wait_all();
+  if (lane == 0) ptx::bulk_wait_all();
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- kernel
@@ -999,7 +1018,7 @@ __device__ __forceinline__ void tg_product(const TgParams& p, const TgFactors& f
   } else if (warp == 3) {
     tg_schedule<Mode>(p, s, at, first, end, step);
   } else {
-    tg_epilogue<Epi, T>(p, f, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
+    tg_epilogue<Mode, Epi, T>(p, f, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
   }
   __syncwarp();
 }
