@@ -487,7 +487,8 @@ int moe_plan_forward_launches(moe_plan_t plan, int fp8);
  * Tensors are bf16 or fp16 (`dtype`; MOE_DTYPE_FP32 where stated), device
  * memory, 16-byte aligned, the last index contiguous. A row pitch (ldx, ldy,
  * ...) is given in elements: at least the row's length and a multiple of 8.
- * K and N are multiples of 8 (rows of whole 16-byte chunks). Products are
+ * K and N are multiples of 8 (rows of whole 16-byte chunks); no extent exceeds
+ * 2^30. Products are
  * accumulated in fp32 on the tensor cores; a result is rounded once, to nearest.
  *
  * error_word: device int32 [1], or NULL. It is zeroed by the call and receives
@@ -496,7 +497,7 @@ int moe_plan_forward_launches(moe_plan_t plan, int fp8);
  *
  * Common errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad pitch,
  * unknown type or activation, negative count), MOE_ERR_UNSUPPORTED_SHAPE (K or N
- * not a multiple of 8, too many groups), MOE_ERR_UNSUPPORTED_DEVICE, MOE_ERR_CUDA. */
+ * not a multiple of 8, an extent or a number of groups too large), MOE_ERR_UNSUPPORTED_DEVICE, MOE_ERR_CUDA. */
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2 } moe_dtype;
 typedef enum {
   MOE_ACT_NONE = 0,

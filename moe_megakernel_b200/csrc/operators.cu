@@ -160,11 +160,15 @@ int launch_pass(void (*kernel)(P), dim3 grid, const P& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+constexpr int kMaxExtent = 1 << 30;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool operand_ok(const void* p) { return p != nullptr && aligned(p, 16); }
 bool pitch_ok(long long ld, int width) { return ld >= width && ld % 8 == 0 && ld < (1ll << 36); }
-// K and N of a product: rows of 16-byte multiples
-bool extents_ok(int K, int N) { return K >= 8 && N >= 8 && K % 8 == 0 && N % 8 == 0; }
+// K and N of a product: rows of 16-byte multiples; all extents leave room for a tile in 32 bits
+bool extents_ok(int K, int N, int rows) {
+  return K >= 8 && N >= 8 && K % 8 == 0 && N % 8 == 0 && K <= kMaxExtent && N <= kMaxExtent && rows <= kMaxExtent;
+}
 bool half_type(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16; }
 
 int clear_error_word(int32_t* err, cudaStream_t st) {
@@ -384,7 +388,7 @@ extern "C" int moe_grouped_matmul(const void* x, long long ldx, const void* W, c
                                   int groups, int K, int N, int transpose, int dtype, void* y, long long ldy,
                                   int32_t* error_word, void* stream) {
   if (rows < 0 || groups < 1 || !half_type(dtype) || !aligned(error_word, 4)) return MOE_ERR_INVALID_ARG;
-  if (!extents_ok(K, N) || groups > kTgMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!extents_ok(K, N, rows) || groups > kTgMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!pitch_ok(ldx, K) || !pitch_ok(ldy, N)) return MOE_ERR_INVALID_ARG;
   if (offsets == nullptr || !aligned(offsets, 4) || !operand_ok(W)) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!operand_ok(x) || !operand_ok(y))) return MOE_ERR_INVALID_ARG;
@@ -402,7 +406,7 @@ extern "C" int moe_grouped_matmul_wgrad(const void* x, long long ldx, const void
                                         const int32_t* offsets, int rows, int groups, int K, int N, int dtype, void* dW,
                                         int32_t* error_word, void* stream) {
   if (rows < 0 || groups < 1 || !half_type(dtype) || !aligned(error_word, 4)) return MOE_ERR_INVALID_ARG;
-  if (!extents_ok(K, N) || groups > kTgMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!extents_ok(K, N, rows) || groups > kTgMaxGroups) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!pitch_ok(ldx, K) || !pitch_ok(lddy, N)) return MOE_ERR_INVALID_ARG;
   if (offsets == nullptr || !aligned(offsets, 4) || !operand_ok(dW)) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!operand_ok(x) || !operand_ok(dy))) return MOE_ERR_INVALID_ARG;
@@ -422,7 +426,7 @@ extern "C" int moe_linear(const void* x, long long ldx, const void* W, const voi
                           void* preact, long long ldz, int32_t* error_word, void* stream) {
   if (T < 0 || !half_type(dtype) || activation < MOE_ACT_NONE || activation > MOE_ACT_SILU || !aligned(error_word, 4))
     return MOE_ERR_INVALID_ARG;
-  if (!extents_ok(K, N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!extents_ok(K, N, T)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!pitch_ok(ldx, K) || !pitch_ok(ldy, N)) return MOE_ERR_INVALID_ARG;
   if (!operand_ok(W) || !aligned(bias, 16)) return MOE_ERR_INVALID_ARG;
   if (residual != nullptr && (!aligned(residual, 16) || !pitch_ok(ldr, N))) return MOE_ERR_INVALID_ARG;
@@ -454,7 +458,7 @@ extern "C" int moe_linear_backward(const void* dy, long long lddy, const void* x
                                    size_t workspace_bytes, int32_t* error_word, void* stream) {
   if (T < 0 || !half_type(dtype) || activation < MOE_ACT_NONE || activation > MOE_ACT_SILU || !aligned(error_word, 4))
     return MOE_ERR_INVALID_ARG;
-  if (!extents_ok(K, N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!extents_ok(K, N, T)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const bool act = activation != MOE_ACT_NONE;
   if (!pitch_ok(lddy, N) || (act && !pitch_ok(ldz, N))) return MOE_ERR_INVALID_ARG;
   if (dx != nullptr && (!pitch_ok(lddx, K) || !aligned(dx, 16) || !operand_ok(W))) return MOE_ERR_INVALID_ARG;

@@ -11,6 +11,7 @@ one element, receives the call's device error code (0 = none).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Union
 
 import torch
@@ -42,7 +43,12 @@ def _like(t, name: str, shape, dtype, device):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    raise ValueError(f"{name}: the last index must be contiguous")
+    _last(t, name)
+
+
+def _last(t, name: str):
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last index must be contiguous")
 
 
 def _whole(t, name: str, shape, dtype, device):
@@ -53,10 +59,9 @@ def _whole(t, name: str, shape, dtype, device):
 
 def _pitch(t, name: str) -> int:
     """Row pitch in elements of a [rows, width] tensor; a single row has its own width."""
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    ld = t.stride(0)
-    if ld < t.shape[1] or ld % 8:
+    rows, width = t.shape
+    ld = t.stride(0) if rows > 1 else width
+    if rows > 1 and (ld < width or ld % 8):
         raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap (stride {ld})")
     return ld
 
@@ -117,10 +122,11 @@ def _workspace(nbytes: int, device, stream):
 
 def _offsets(offsets, device):
     _tensor(offsets, "offsets", 1)
-    if offsets.shape[0] < 2:
+    groups = offsets.shape[0] - 1
+    if groups < 1:
         raise ValueError("offsets: expected groups + 1 >= 2 values")
-    _whole(offsets, "offsets", offsets.shape, torch.int32, device)
-    return offsets.shape[0] - 1
+    _whole(offsets, "offsets", (groups + 1,), torch.int32, device)
+    return groups
 
 
 def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, transpose: bool = False,
@@ -139,11 +145,11 @@ def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, tran
     dev = x.device
     groups = _offsets(offsets, dev)
     N = W.shape[1] if transpose else W.shape[2]
-    _like(x, "x", (rows, K), x.dtype, dev)
+    _last(x, "x")
     _whole(W, "W", (groups, N, K) if transpose else (groups, K, N), x.dtype, dev)
     _cuda(x, "x")
     if y is None:
-        y = torch.empty((rows, N), dtype=x.dtype, device=dev)
+        y = x.new_empty((rows, N))
     else:
         _like(y, "y", (rows, N), x.dtype, dev)
     _call("moe_grouped_matmul", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), offsets.data_ptr(), rows, groups, K, N,
@@ -164,11 +170,11 @@ def grouped_matmul_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tenso
     N = dy.shape[1]
     dev = x.device
     groups = _offsets(offsets, dev)
-    _like(x, "x", (rows, K), x.dtype, dev)
+    _last(x, "x")
     _like(dy, "dy", (rows, N), x.dtype, dev)
     _cuda(x, "x")
     if dW is None:
-        dW = torch.empty((groups, K, N), dtype=x.dtype, device=dev)
+        dW = x.new_empty((groups, K, N))
     else:
         _whole(dW, "dW", (groups, K, N), x.dtype, dev)
     _call("moe_grouped_matmul_wgrad", dev, x.data_ptr(), _pitch(x, "x"), dy.data_ptr(), _pitch(dy, "dy"),
@@ -191,7 +197,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     T, K = x.shape
     N = W.shape[1]
     dev = x.device
-    _like(x, "x", (T, K), x.dtype, dev)
+    _last(x, "x")
     _whole(W, "W", (K, N), x.dtype, dev)
     if bias is not None:
         _whole(bias, "bias", (N,), x.dtype, dev)
@@ -199,13 +205,13 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
         _like(residual, "residual", (T, N), x.dtype, dev)
     _cuda(x, "x")
     if y is None:
-        y = torch.empty((T, N), dtype=x.dtype, device=dev)
+        y = x.new_empty((T, N))
     else:
         _like(y, "y", (T, N), x.dtype, dev)
     if preact is not None:
         _like(preact, "preact", (T, N), x.dtype, dev)
     elif save_preact:
-        preact = torch.empty((T, N), dtype=x.dtype, device=dev)
+        preact = x.new_empty((T, N))
     _call("moe_linear", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), _address(bias), _address(residual),
           0 if residual is None else _pitch(residual, "residual"), T, K, N, act, dt, y.data_ptr(), _pitch(y, "y"),
           _address(preact), 0 if preact is None else _pitch(preact, "preact"), _error_word(error_word, dev),
@@ -226,7 +232,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, preact: 
     T, K = x.shape
     N = W.shape[1]
     dev = x.device
-    _like(x, "x", (T, K), x.dtype, dev)
+    _last(x, "x")
     _whole(W, "W", (K, N), x.dtype, dev)
     _like(dy, "dy", (T, N), x.dtype, dev)
     if act and preact is None:
@@ -236,15 +242,24 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, preact: 
         _like(z, "preact", (T, N), x.dtype, dev)
     _cuda(x, "x")
     lib = load_library()
-    dx = torch.empty((T, K), dtype=x.dtype, device=dev) if input_grad else None
-    dW = torch.empty((K, N), dtype=x.dtype, device=dev) if weight_grad else None
-    dbias = torch.empty((N,), dtype=x.dtype, device=dev) if bias_grad else None
+    dx = x.new_empty((T, K)) if input_grad else None
+    dW = x.new_empty((K, N)) if weight_grad else None
+    dbias = x.new_empty((N,)) if bias_grad else None
     nbytes = lib.moe_linear_backward_workspace_bytes(T, N, act, 1 if bias_grad else 0)
     ws = _workspace(nbytes, dev, stream)
     _call("moe_linear_backward", dev, dy.data_ptr(), _pitch(dy, "dy"), x.data_ptr(), _pitch(x, "x"), W.data_ptr(),
           _address(z), 0 if z is None else _pitch(z, "preact"), T, K, N, act, dt, _address(dx), K, _address(dW),
           _address(dbias), _address(ws), nbytes, _error_word(error_word, dev), _raw_stream(stream, dev))
     return dict(dx=dx, dW=dW, dbias=dbias)
+
+
+@functools.lru_cache(maxsize=64)
+def _schedule(steps: int, coeffs: tuple):
+    """The steps' coefficients as the C array [steps, 3] (read during the call only)."""
+    rows = list(coeffs) if coeffs and isinstance(coeffs[0], tuple) else [coeffs] * steps
+    if len(rows) != steps or any(not isinstance(r, tuple) or len(r) != 3 for r in rows):
+        raise ValueError("coeffs: expected (a, b, c), or one such triple for each step")
+    return (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
 
 
 def orthogonalize(G: torch.Tensor, steps: int = 5,
@@ -264,15 +279,14 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
         raise ValueError(f"G: expected bfloat16 or float32, got {G.dtype}")
     if steps < 1:
         raise ValueError("steps must be at least 1")
-    rows = [list(c) for c in coeffs] if isinstance(coeffs[0], (list, tuple)) else [list(coeffs)] * steps
-    if len(rows) != steps or any(len(r) != 3 for r in rows):
-        raise ValueError("coeffs: expected (a, b, c), or one such triple for each step")
-    _like(G, "G", G.shape, G.dtype, G.device)
+    flat = _schedule(steps, tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coeffs))
+    _last(G, "G")
     _cuda(G, "G")
     dev = G.device
     if out is None:
         out = torch.empty(G.shape, dtype=torch.bfloat16, device=dev)
-    _like(out, "out", G.shape, torch.bfloat16, dev)
+    else:
+        _like(out, "out", tuple(G.shape), torch.bfloat16, dev)
 
     def pitches(t, name):
         t = t if t.dim() == 3 else t.unsqueeze(0)
@@ -284,7 +298,6 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
 
     batch, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
     lib = load_library()
-    flat = (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
     nbytes = lib.moe_orthogonalize_workspace_bytes(batch, m, n)
     ws = _workspace(nbytes, dev, stream)
     _call("moe_orthogonalize", dev, G.data_ptr(), *pitches(G, "G"), batch, m, n, DTYPE_CODES[G.dtype], steps, flat, eps,

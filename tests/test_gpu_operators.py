@@ -87,6 +87,25 @@ def test_grouped_rows_outside_the_groups_stay_and_do_not_spread():
         close(y[lo:hi], x[lo:hi].double() @ W[e].double(), x[lo:hi].double().abs() @ W[e].double().abs(), K)
 
 
+def test_grouped_strided_rows_and_many_groups():
+    """Row pitches beyond the row, and the most groups a call takes, most of them empty."""
+    K, N, groups = 72, 88, 1024
+    g = torch.Generator().manual_seed(0)
+    counts = [int(c) if i % 5 == 0 else 0 for i, c in enumerate(torch.randint(0, 40, (groups,), generator=g))]
+    counts[groups - 1] = 41
+    off, rows = offsets_of(counts), sum(counts)
+    xs, ys = rand(rows, K + 16, seed=17), torch.full((rows, N + 24), 3.25, dtype=BF, device="cuda")
+    x, y = xs[:, 8:8 + K], ys[:, 16:16 + N]
+    W = rand(groups, K, N, seed=18, std=K ** -0.5)
+    mk.grouped_matmul(x, W, off, y=y)
+    dW = mk.grouped_matmul_wgrad(x, y, off)
+    assert (ys[:, :16] == 3.25).all() and (ys[:, 16 + N:] == 3.25).all()
+    for e, lo, hi in spans(off):
+        a, b = x[lo:hi].double(), y[lo:hi].double()
+        close(y[lo:hi], a @ W[e].double(), a.abs() @ W[e].double().abs(), K, f"group {e}")
+        close(dW[e], a.T @ b, a.abs().T @ b.abs(), hi - lo, f"dW {e}")
+
+
 @pytest.mark.parametrize("bad", [[0, 5, 3, 9], [-1, 2, 4, 9], [0, 4, 6, 99]])
 def test_grouped_bad_offsets_are_recorded_and_skipped(bad):
     K, N = 64, 64
@@ -195,6 +214,9 @@ def slope64(z, act):
     (33, 2056, 96, "gelu_tanh", True, False, True), (64, 136, 4104, None, True, True, True),
     (65, 64, 64, "silu", False, False, True), (128, 328, 640, "gelu", True, True, True),
     (129, 8, 8, "relu", True, True, True), (300, 584, 776, "silu", True, True, False),
+    (37, 8192, 264, "gelu", True, True, True), (200, 4096, 512, "silu", True, True, True),
+    (500, 6000, 136, None, True, True, True), (31, 320, 40000, "relu", True, False, False),
+    (2100, 136, 1288, "gelu", True, True, True),
     (1031, 256, 520, "gelu", True, False, True)])
 def test_linear(T, K, N, act, bias, res, save, dtype):
     x, W = rand(T, K, seed=21, dtype=dtype), rand(K, N, seed=22, dtype=dtype, std=K ** -0.5)
@@ -236,7 +258,8 @@ def test_linear_onto_the_residual_itself_and_strided_rows():
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("T,K,N,act,bias", [
     (1, 64, 128, "silu", True), (5, 8, 8, None, True), (37, 520, 264, "gelu", True), (128, 136, 1032, "relu", False),
-    (200, 256, 256, "gelu_tanh", True), (1031, 328, 520, "silu", True), (4100, 64, 72, None, True)])
+    (200, 256, 256, "gelu_tanh", True), (1031, 328, 520, "silu", True), (4100, 64, 72, None, True),
+    (64, 256, 4096, "gelu", True), (150, 520, 6000, "silu", False)])
 def test_linear_backward(T, K, N, act, bias, dtype):
     x, W = rand(T, K, seed=41, dtype=dtype), rand(K, N, seed=42, dtype=dtype, std=K ** -0.5)
     dy = rand(T, N, seed=43, dtype=dtype, std=0.2)
@@ -317,7 +340,8 @@ def gradient(*shape, seed, dtype=torch.float32, rank=4):
 
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (5, 3), (33, 64), (64, 33), (129, 250), (250, 129),
-                                   (256, 256), (3, 130, 70), (5, 40, 300), (2, 513, 257), (300, 1031), (1000, 520)])
+                                   (256, 256), (3, 130, 70), (5, 40, 300), (2, 513, 257), (300, 1031), (1000, 520),
+                                   (40, 300, 520), (40, 520, 300), (90, 130, 140), (300, 20, 33)])
 def test_orthogonalize(shape, dtype):
     G = gradient(*shape, seed=61, dtype=dtype, rank=min(4, *shape[-2:]))
     ortho_close(mk.orthogonalize(G), G)
@@ -423,6 +447,57 @@ def test_two_streams_and_captured_graphs():
     torch.cuda.synchronize()
     for g in outs:
         assert all(torch.equal(a, b) for a, b in zip(ref, g))
+
+
+def test_offsets_past_32_bits():
+    """A weight set and an activation whose element offsets pass 2^31."""
+    K, N, groups = 4096, 8192, 70                      # 70 x 33.5 M = 2.35e9 elements
+    W = torch.zeros(groups, K, N, dtype=BF, device="cuda")
+    W[groups - 1] = rand(K, N, seed=111, std=K ** -0.5)
+    off = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    off[groups] = 50
+    x = rand(50, K, seed=112)
+    y = mk.grouped_matmul(x, W, off)
+    ref, S = x.double() @ W[-1].double(), x.double().abs() @ W[-1].double().abs()
+    close(y, ref, S, K)
+    dW = mk.grouped_matmul_wgrad(x, y, off, dW=W)
+    assert (dW[:groups - 1] == 0).all()
+    close(dW[-1], x.double().T @ y.double(), x.double().abs().T @ y.double().abs(), 50)
+    del W, dW
+    T, K, N = 280_000, 64, 8192                        # 2.29e9 outputs
+    x, W = rand(T, K, seed=113), rand(K, N, seed=114, std=0.125)
+    y = mk.linear(x, W)
+    tail = slice(T - 300, T)
+    close(y[tail], x[tail].double() @ W.double(), x[tail].double().abs() @ W.double().abs(), K)
+
+
+def test_orthogonalized_steps_of_a_training_loop():
+    """Two steps of a dense layer trained with orthogonalised updates, all captured in one graph: every
+    replay moves the weights as the same calls outside the graph do."""
+    T, K, N = 200, 128, 264
+    x, t = rand(T, K, seed=121), rand(T, N, seed=122)
+    W0, b0 = rand(K, N, seed=123, std=K ** -0.5), rand(N, seed=124, std=0.1)
+
+    def step(W, b):
+        y, z = mk.linear(x, W, bias=b, activation="silu", save_preact=True)
+        g = mk.linear_backward(y - t, x, W, preact=z, activation="silu", bias_grad=True)
+        W.sub_(mk.orthogonalize(g["dW"]), alpha=0.02)
+        b.sub_(g["dbias"], alpha=1e-3)
+
+    Wa, ba = W0.clone(), b0.clone()
+    for _ in range(3):
+        step(Wa, ba)
+        step(Wa, ba)
+    Wg, bg = W0.clone(), b0.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(Wg, bg)
+        step(Wg, bg)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Wa, Wg) and torch.equal(ba, bg)
+    assert not torch.equal(Wg, W0)
 
 
 def test_layer_from_its_parts():

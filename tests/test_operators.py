@@ -31,7 +31,7 @@ GROUPED = dict(x=A, ldx=64, W=A, offsets=A, rows=10, groups=4, K=64, N=128, tran
     (dict(x=None), 1), (dict(x=ODD), 1), (dict(W=None), 1), (dict(W=ODD), 1), (dict(offsets=None), 1),
     (dict(y=None), 1), (dict(y=ODD), 1), (dict(rows=-1), 1), (dict(groups=0), 1), (dict(groups=1025), 2),
     (dict(K=60, ldx=64), 2), (dict(N=100), 2), (dict(K=0), 2), (dict(ldx=56), 1), (dict(ldx=68), 1), (dict(ldy=120), 1),
-    (dict(dtype=2), 1), (dict(dtype=7), 1), (dict(error_word=ctypes.c_void_p(6)), 1)])
+    (dict(rows=(1 << 30) + 1), 2), (dict(dtype=2), 1), (dict(dtype=7), 1), (dict(error_word=ctypes.c_void_p(6)), 1)])
 def test_grouped_matmul_refusals(lib, change, status):
     assert lib.moe_grouped_matmul(*(GROUPED | change).values()) == status
 
@@ -55,7 +55,8 @@ LINEAR = dict(x=A, ldx=64, W=A, bias=None, residual=None, ldr=0, T=3, K=64, N=12
 @pytest.mark.parametrize("change,status", [
     (dict(x=None), 1), (dict(W=None), 1), (dict(y=None), 1), (dict(bias=ODD), 1), (dict(residual=A, ldr=64), 1),
     (dict(residual=ODD, ldr=128), 1), (dict(preact=A, ldz=0), 1), (dict(T=-1), 1), (dict(activation=5), 1),
-    (dict(activation=-1), 1), (dict(dtype=2), 1), (dict(K=20), 2), (dict(N=4), 2)])
+    (dict(activation=-1), 1), (dict(dtype=2), 1), (dict(K=20), 2), (dict(N=4), 2),
+    (dict(T=2 ** 31 - 1), 2)])
 def test_linear_refusals(lib, change, status):
     assert lib.moe_linear(*(LINEAR | change).values()) == status
 
