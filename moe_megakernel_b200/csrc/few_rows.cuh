@@ -1,12 +1,14 @@
-// y = act(x W + bias) + residual for few rows of x (serving: one token to some hundred):
-// the time is that of reading W once, so the work is cut for the memory system.
-// A CTA holds 128 output features (the MMA's M rows) and up to 128 tokens (its N
-// columns); the reduction is split over the S CTAs of a cluster so that about
-// two CTAs run on every SM whatever N is, each with some 100 KB of W in flight.
-// The S partial tiles meet in distributed shared memory: every CTA leaves its
-// fp32 tile in its own shared memory, and after a cluster barrier adds up its
-// 1/S of the entries over the peers, in rank order, so a result does not depend
-// on timing and no workspace or counter is needed.
+// Products of few tiles: y = act(x W + bias) + residual for few rows of x
+// (serving: one token to some hundred), where the time is that of reading W once,
+// and products whose reduction is long for their size (a weight gradient of a
+// small layer over thousands of rows). A CTA holds 128 output features (the MMA's
+// M rows) and up to 128 tokens (its N columns); the reduction is split over the S
+// CTAs of a cluster so that about two CTAs run on every SM whatever the sizes
+// are, each with some 100 KB of operands in flight. The S partial tiles meet in
+// distributed shared memory: every CTA leaves its fp32 tile in its own shared
+// memory, and after a cluster barrier adds up its 1/S of the entries over the
+// peers, in rank order, so a result does not depend on timing and no workspace
+// or counter is needed.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -15,14 +17,13 @@
 namespace moe {
 
 constexpr int kFewThreads = 192;   // warp 0 TMA, warp 1 MMA and TMEM, warps 2..5 the partial tile
-constexpr int kFewMaxRows = 512;   // beyond this the pairs are always as fast
 constexpr int kFewMaxStages = 6;
 constexpr int kFewMaxSplit = 8;    // portable cluster size
 constexpr int kFewSmemTiles = 108 * 1024;   // two CTAs on an SM
 
 struct FewParams {
   CUtensorMap tm_w;   // MN-major: {n, k} box {64, 64}; K-major: {k, n} box {64, 128}
-  CUtensorMap tm_x;   // {k, t} box {64, nt}
+  CUtensorMap tm_x;   // K-major: {k, t} box {64, nt}; MN-major: {t, k} box {64, 64}
   int M, K, T;        // output features, reduction, tokens
   int nt;             // MMA columns: 32, 64 or 128
   int split, stages;
@@ -119,7 +120,7 @@ __device__ __forceinline__ void few_finish(const FewParams& p, float4 a, long lo
       make_uint2(TgPair<T>::pack(a.x, a.y), TgPair<T>::pack(a.z, a.w));
 }
 
-template <bool PMn, typename T>
+template <bool PMn, bool QMn, typename T>
 __global__ void __launch_bounds__(kFewThreads, 2) moe_few_rows_kernel(const __grid_constant__ FewParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -170,7 +171,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) moe_few_rows_kernel(const __gr
         } else {
           few_load3(dst, &p.tm_w, &s.full[stage], kb * 64, m0);
         }
-        few_load3(dst + kTgABytes, &p.tm_x, &s.full[stage], kb * 64, t0);
+        if (QMn) {
+          for (int j = 0; j < p.nt; j += 64) few_load3(dst + kTgABytes + j * 128, &p.tm_x, &s.full[stage], t0 + j, kb * 64);
+        } else {
+          few_load3(dst + kTgABytes, &p.tm_x, &s.full[stage], kb * 64, t0);
+        }
       }
       __syncwarp();
       if (++stage == p.stages) {
@@ -182,11 +187,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) moe_few_rows_kernel(const __gr
       for (int i = 0; i < 5000; ++i) __nanosleep(1000);
   } else if (warp == 1) {
     const uint32_t fmt = p.f16 ? 0u : 1u;
-    const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((PMn ? 1u : 0u) << 15) | ((uint32_t)(p.nt >> 3) << 17) |
+    const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((PMn ? 1u : 0u) << 15) | ((QMn ? 1u : 0u) << 16) |
+                           ((uint32_t)(p.nt >> 3) << 17) |
                            ((128u >> 4) << 24);
     const uint64_t pdesc = PMn ? ptx::smem_desc_sw128(base, 8192, 1024) : ptx::smem_desc_sw128(base, 16, 1024);
-    const uint64_t qdesc = ptx::smem_desc_sw128(base + kTgABytes, 16, 1024);
-    constexpr uint64_t pstep = (PMn ? 2048 : 32) >> 4, qstep = 32 >> 4;
+    const uint64_t qdesc = QMn ? ptx::smem_desc_sw128(base + kTgABytes, 8192, 1024)
+                               : ptx::smem_desc_sw128(base + kTgABytes, 16, 1024);
+    constexpr uint64_t pstep = (PMn ? 2048 : 32) >> 4, qstep = (QMn ? 2048 : 32) >> 4;
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -198,10 +199,23 @@ int pick_tile(long long rows, int mt, int batch, int pairs, bool q_mn) {
 }
 
 // N tile of a ragged product: twice the mean rows of a group, so that most
-// groups are one tile and the stages of a launch with few rows are small.
-int ragged_tile(int rows, int groups) {
+// groups are one tile and the stages of a launch with few rows are small; and
+// less where the tiles would leave pairs idle (taking every group to end in half
+// a tile, with the costs of pick_tile).
+int ragged_tile(int rows, int groups, int mt, int pairs) {
   const int mean = (rows + groups - 1) / groups;
-  return mean <= 16 ? 32 : mean <= 32 ? 64 : mean <= 64 ? 128 : 256;
+  const int most = mean <= 16 ? 32 : mean <= 32 ? 64 : mean <= 64 ? 128 : 256;
+  int best = most;
+  long long least = -1;
+  for (int nt = most; nt >= 32; nt /= 2) {
+    const long long tiles = ((long long)rows / nt + (groups + 1) / 2) * mt;
+    const long long cost = (tiles + pairs - 1) / pairs * (256 + nt);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = nt;
+    }
+  }
+  return best;
 }
 
 template <bool PMn>
@@ -228,9 +242,11 @@ struct FewCut {
   int nt, split;
   double us;
 };
-FewCut few_cut(int T, int M, int K, int sms) {
-  FewCut best{T <= 32 ? 32 : T <= 64 ? 64 : 128, 1, 1e30};
-  const long long cells = (long long)((M + 127) / 128) * ((T + best.nt - 1) / best.nt);
+FewCut few_cut(int T, int M, int K, int sms, bool q_mn) {
+  FewCut best{T <= 32 && !q_mn ? 32 : T <= 64 ? 64 : 128, 1, 1e30};   // an MN-major Q comes in boxes of 64
+  const int across = (T + best.nt - 1) / best.nt;
+  if (across > 65535) return best;   // the grid's second extent
+  const long long cells = (long long)((M + 127) / 128) * across;
   const int nk = (K + 63) / 64;
   for (int c = 1; c <= kFewMaxSplit && c <= std::max(1, nk / 2); ++c) {
     const double rounds = (double)((cells * c + 2 * sms - 1) / (2 * sms));
@@ -243,12 +259,12 @@ double pairs_us(long long tiles, int nt, int K, int pairs) {
   return (double)((tiles + pairs - 1) / pairs) * ((K + 63) / 64 * std::max(0.27, nt * 0.0011) + 3.0);
 }
 
-template <bool PMn, typename T>
+template <bool PMn, bool QMn, typename T>
 int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Operand& Q, cudaStream_t st) {
   static std::atomic<int> ready[kMaxDevices];
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return MOE_ERR_CUDA;
-  auto kernel = moe_few_rows_kernel<PMn, T>;
+  auto kernel = moe_few_rows_kernel<PMn, QMn, T>;
   if (!ready[d].load()) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kFewSmemTiles + 1024 + sizeof(FewSmem))) != cudaSuccess)
@@ -272,7 +288,7 @@ int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Ope
   f.z = p.z;
   f.ldz = p.ldz;
   f.act = p.act;
-  if (!map3(&f.tm_w, P, PMn ? 64 : 128, p.f16 != 0) || !map3(&f.tm_x, Q, f.nt, p.f16 != 0)) return MOE_ERR_CUDA;
+  if (!map3(&f.tm_w, P, PMn ? 64 : 128, p.f16 != 0) || !map3(&f.tm_x, Q, QMn ? 64 : f.nt, p.f16 != 0)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -305,21 +321,22 @@ int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int r
     p.nt = pick_tile(rows, mt, 1, std::max(1, sms / 2), false);
     tiles = (long long)((rows + p.nt - 1) / p.nt) * mt;
   } else {
-    p.nt = ragged_tile(rows, groups);
+    p.nt = ragged_tile(rows, groups, mt, std::max(1, sms / 2));
   }
   if (((long long)rows / 32 + groups) * mt >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const Operand P = transpose ? Operand{W, (uint64_t)K, (uint64_t)N, (uint64_t)K, (uint64_t)groups, (uint64_t)K * N}
                               : Operand{W, (uint64_t)N, (uint64_t)K, (uint64_t)N, (uint64_t)groups, (uint64_t)K * N};
   const Operand Q{x, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 1, 0};
-  if (p.offsets == nullptr && rows <= kFewMaxRows) {
+  if (p.offsets == nullptr) {
     if (sms < 0) return MOE_ERR_UNSUPPORTED_DEVICE;
-    const FewCut cut = few_cut(rows, N, K, sms);
+    const FewCut cut = few_cut(rows, N, K, sms, false);
     p.out = y;
     p.ldo = ldy;
     if (cut.us < pairs_us(tiles, p.nt, K, std::max(1, sms / 2))) {
       if (dtype == MOE_DTYPE_FP16)
-        return transpose ? launch_few<false, __half>(p, cut, P, Q, st) : launch_few<true, __half>(p, cut, P, Q, st);
-      return transpose ? launch_few<false, bf16>(p, cut, P, Q, st) : launch_few<true, bf16>(p, cut, P, Q, st);
+        return transpose ? launch_few<false, false, __half>(p, cut, P, Q, st)
+                         : launch_few<true, false, __half>(p, cut, P, Q, st);
+      return transpose ? launch_few<false, false, bf16>(p, cut, P, Q, st) : launch_few<true, false, bf16>(p, cut, P, Q, st);
     }
   }
   if (!set_maps(p, P, !transpose, Q, false) || !set_out(p, y, N, rows, ldy, 1, 0)) return MOE_ERR_CUDA;
@@ -342,6 +359,18 @@ int weight_gradient(TgParams& p, const void* x, long long ldx, const void* dy, l
   if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const Operand P{dy, (uint64_t)N, (uint64_t)rows, (uint64_t)lddy, 1, 0};
   const Operand Q{x, (uint64_t)K, (uint64_t)rows, (uint64_t)ldx, 1, 0};
+  if (p.offsets == nullptr) {   // few tiles: the reduction over the rows is split
+    if (sms < 0) return MOE_ERR_UNSUPPORTED_DEVICE;
+    const FewCut cut = few_cut(K, N, rows, sms, true);
+    if (cut.us < pairs_us(tiles, p.nt, rows, std::max(1, sms / 2))) {
+      p.out = dW;
+      p.ldo = N;
+      p.N = K;
+      p.K = rows;
+      return dtype == MOE_DTYPE_FP16 ? launch_few<true, true, __half>(p, cut, P, Q, st)
+                                     : launch_few<true, true, bf16>(p, cut, P, Q, st);
+    }
+  }
   if (!set_maps(p, P, true, Q, true) || !set_out(p, dW, N, K, N, groups, (uint64_t)K * N)) return MOE_ERR_CUDA;
   return launch_wgrad(p, dtype, tiles, st);
 }
@@ -611,12 +640,22 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     return MOE_ERR_CUDA;
   const long long tiles = (long long)((m + g4.nt - 1) / g4.nt) * ((n + 255) / 256) * batch;
   if (tri >= (1ll << 30) || tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // B is stored less a multiple d of the identity, X' = (a + d) X + (B - d I) X: once the singular values are
+  // near 1, B's eigenvalues lie within a few tenths of b + c = -2.7, and the fp16 roundings of B and X enter X'
+  // times what is left of B. d is B's eigenvalue at the root mean square of the singular values, which starts
+  // at 1 / sqrt(p) and is followed through the steps (a guess: any d is exact up to rounding). Error against
+  // 64 bits of a 28 x 1835 matrix without it 2.5e-3, of which bf16's own rounding is 1.7e-3.
+  double sigma = 1.0 / std::sqrt((double)p0);
   for (int i = 0; i < steps; ++i) {
+    const double ca = coeffs[3 * i], cb = coeffs[3 * i + 1], cc = coeffs[3 * i + 2];
+    const double t = std::min(1.0, sigma * sigma);
+    const float d = (float)(cb * t + cc * t * t);
+    sigma = std::fabs(sigma * (ca + cb * sigma * sigma + cc * sigma * sigma * sigma * sigma));
     const bool last = i == steps - 1;
     const float* alpha = i == 0 ? o.alpha : nullptr;
     TgParams& a = g1[i & 1];
     a.factors.alpha = alpha;
-    g2.factors = TgFactors{coeffs[3 * i + 1], coeffs[3 * i + 2] / as, nullptr, nullptr};
+    g2.factors = TgFactors{coeffs[3 * i + 1], coeffs[3 * i + 2] / as, nullptr, nullptr, -d * as};
     int rc;
     if (half) {
       rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(a, tri, st)
@@ -631,7 +670,7 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     if (rc) return rc;
     TgParams& x = last ? g4 : g3[i & 1];
     const float back = last ? 1.f / xs : 1.f;
-    x.factors = TgFactors{coeffs[3 * i] * back, back / as, alpha, i == 0 ? lo_first : ws + L.lo};
+    x.factors = TgFactors{(coeffs[3 * i] + d) * back, back / as, alpha, i == 0 ? lo_first : ws + L.lo, 0.f};
     if (tall)
       rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(x, tiles, st)
                 : launch<kTgBatched, false, false, kTgUpdate, __half>(x, tiles, st);

@@ -64,6 +64,7 @@ struct TgFactors {
   float ca, cb;           // on the stored value and on the accumulator
   const float* alpha;     // [batches] or null: times the update, squared times the Gram matrix
   const uint8_t* lo_in;   // the low bits of X, or null
+  float diagonal;         // kTgPoly: added to the diagonal
 };
 
 struct TgParams {
@@ -747,7 +748,8 @@ __device__ __forceinline__ long long tg_low_at(const TgParams& p, const TgTask& 
 template <int Epi, typename T>
 __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][16], uint32_t (&v)[16],
                                                uint32_t (&lo)[8], const TgParams& p, const TgTask& k, int c, int m,
-                                               int lane, const float (&bias)[4], float ca, float cb) {
+                                               int lane, const float (&bias)[4], float ca, float cb,
+                                               float diagonal) {
   if (Epi == kTgStore) {
     uint32_t res[16];
     if (p.res != nullptr) tg_piece_get<kRowsN>(slot, res, lane);
@@ -795,6 +797,10 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
           const float2 f = TgPair<__half>::unpack(v[4 * i + b]);
           x += ca * f.x;
           y += ca * f.y;
+          if (i == b && m == k.n0 + c * 32) {
+            if ((lane >> 2) == 2 * (lane & 3)) x += diagonal;
+            if ((lane >> 2) == 2 * (lane & 3) + 1) y += diagonal;
+          }
         }
         v[4 * i + b] = TgPair<__half>::pack(x, y);
       }
@@ -946,7 +952,7 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
       }
-      tg_piece_value<Epi, T>(slot, r, v, lo, p, k, c, m, lane, bias, ca, cb);
+      tg_piece_value<Epi, T>(slot, r, v, lo, p, k, c, m, lane, bias, ca, cb, f.diagonal);
       if (any && again) {
         tg_tmem_frag(from + (c + kParts) * 32, r[0]);
         tg_tmem_frag(from + (c + kParts) * 32 + (16u << 16), r[1]);

@@ -53,7 +53,8 @@ RAGGED = [0, 1, 31, 32, 33, 0, 64, 100, 255, 256, 257, 513, 2, 0]
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("counts,K,N", [
     (RAGGED, 192, 264), (RAGGED, 72, 520), ([1], 8, 8), ([3, 0, 5], 128, 256), ([1] * 40, 200, 328),
-    ([0, 0, 0, 700], 1000, 128), ([20] * 16, 64, 64), ([50] * 9, 328, 96)])
+    ([0, 0, 0, 700], 1000, 128), ([20] * 16, 64, 64), ([50] * 9, 328, 96),
+    ([300, 0, 150, 420, 178], 2000, 352)])
 def test_grouped_matmul(counts, K, N, transpose, dtype):
     off = offsets_of(counts)
     rows = sum(counts)
@@ -259,7 +260,8 @@ def test_linear_onto_the_residual_itself_and_strided_rows():
 @pytest.mark.parametrize("T,K,N,act,bias", [
     (1, 64, 128, "silu", True), (5, 8, 8, None, True), (37, 520, 264, "gelu", True), (128, 136, 1032, "relu", False),
     (200, 256, 256, "gelu_tanh", True), (1031, 328, 520, "silu", True), (4100, 64, 72, None, True),
-    (64, 256, 4096, "gelu", True), (150, 520, 6000, "silu", False)])
+    (64, 256, 4096, "gelu", True), (150, 520, 6000, "silu", False), (3812, 104, 776, None, False),
+    (1598, 664, 256, "silu", True), (2051, 24, 136, "relu", True), (777, 200, 96, "gelu", False)])
 def test_linear_backward(T, K, N, act, bias, dtype):
     x, W = rand(T, K, seed=41, dtype=dtype), rand(K, N, seed=42, dtype=dtype, std=K ** -0.5)
     dy = rand(T, N, seed=43, dtype=dtype, std=0.2)
@@ -341,7 +343,7 @@ def gradient(*shape, seed, dtype=torch.float32, rank=4):
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (5, 3), (33, 64), (64, 33), (129, 250), (250, 129),
                                    (256, 256), (3, 130, 70), (5, 40, 300), (2, 513, 257), (300, 1031), (1000, 520),
-                                   (40, 300, 520), (40, 520, 300), (90, 130, 140), (300, 20, 33)])
+                                   (40, 300, 520), (40, 520, 300), (90, 130, 140), (300, 20, 33), (58, 28, 1835)])
 def test_orthogonalize(shape, dtype):
     G = gradient(*shape, seed=61, dtype=dtype, rank=min(4, *shape[-2:]))
     ortho_close(mk.orthogonalize(G), G)
