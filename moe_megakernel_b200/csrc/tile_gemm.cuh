@@ -707,20 +707,30 @@ __host__ __device__ constexpr int tg_epi_bytes(bool residual) { return kTgEpiWar
 // value. Together 19 bits, so that a X keeps small singular directions beside
 // large ones at 3 bytes an entry. The 8 bits never leave this epilogue and lie
 // in the order its threads hold them: a piece is 32 lanes x 32 bytes.
-__device__ __forceinline__ int tg_low(float x, float h) {
-  const int d = (__float_as_int(x) - __float_as_int(h)) >> 5;
-  return max(-128, min(127, d));
+__device__ __forceinline__ int tg_low(float x, float h) { return (__float_as_int(x) - __float_as_int(h)) >> 5; }
+// Four of them as bytes (saturated: a tie rounded down leaves +128, and below fp16's normal numbers more).
+__device__ __forceinline__ uint32_t tg_low4(int a, int b, int c, int d) {
+  uint32_t hi, all;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(d), "r"(c));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(all) : "r"(b), "r"(a), "r"(hi));
+  return all;
 }
-// hi: two fp16 of which byte pair `half` of w is the low part
+// hi: two fp16 whose low bits are bytes 2 half and 2 half + 1 of w; the dot product with 32 at one byte
+// extends its sign, scales and adds it in one instruction
 __device__ __forceinline__ float2 tg_wide(uint32_t hi, uint32_t w, int half) {
   const float2 f = TgPair<__half>::unpack(hi);
-  int a, b;   // bytes 0 and 1 (2 and 3), sign-extended (bit 3 of a selector repeats the byte's sign)
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(a) : "r"(w), "r"(half ? 0xaaa2 : 0x8880));
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(b) : "r"(w), "r"(half ? 0xbbb3 : 0x9991));
-  return make_float2(__int_as_float(__float_as_int(f.x) + a * 32), __int_as_float(__float_as_int(f.y) + b * 32));
+  return make_float2(__int_as_float(__dp4a((int)w, half ? 0x200000 : 0x20, __float_as_int(f.x))),
+                     __int_as_float(__dp4a((int)w, half ? 0x20000000 : 0x2000, __float_as_int(f.y))));
 }
-__device__ __forceinline__ uint32_t tg_low4(int a, int b, int c, int d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+// a x + b y for two values at once
+__device__ __forceinline__ float2 tg_axpby(float a, float2 x, float b, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, x, y;\n\t"
+      "mov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %3};\n\tmov.b64 x, {%4, %5};\n\tmov.b64 y, {%6, %7};\n\t"
+      "mul.rn.f32x2 y, b, y;\n\tfma.rn.f32x2 y, a, x, y;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
 }
 
 template <int Epi, typename T>
@@ -813,16 +823,15 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
       for (int h = 0; h < 2; ++h) {
         const int i = (j + h) >> 2, b = (j + h) & 3;
         const uint32_t* e = &r[b >> 1][4 * i + 2 * (b & 1)];
-        const float2 old = tg_wide(v[j + h], lo[j >> 1], h);
-        const float x = ca * old.x + cb * __uint_as_float(e[0]);
-        const float y = ca * old.y + cb * __uint_as_float(e[1]);
+        const float2 x = tg_axpby(ca, tg_wide(v[j + h], lo[j >> 1], h), cb,
+                                  make_float2(__uint_as_float(e[0]), __uint_as_float(e[1])));
         if (Epi == kTgUpdate) {
-          v[j + h] = TgPair<__half>::pack(x, y);
+          v[j + h] = TgPair<__half>::pack(x.x, x.y);
           const float2 n = TgPair<__half>::unpack(v[j + h]);
-          q[2 * h] = tg_low(x, n.x);
-          q[2 * h + 1] = tg_low(y, n.y);
+          q[2 * h] = tg_low(x.x, n.x);
+          q[2 * h + 1] = tg_low(x.y, n.y);
         } else {
-          v[j + h] = TgPair<bf16>::pack(x, y);
+          v[j + h] = TgPair<bf16>::pack(x.x, x.y);
         }
       }
       if (Epi == kTgUpdate) lo[j >> 1] = tg_low4(q[0], q[1], q[2], q[3]);
@@ -833,10 +842,10 @@ __device__ __forceinline__ void tg_piece_value(uint32_t slot, uint32_t (&r)[2][1
 // Second half: through `slot` to the output.
 template <int Mode, int Epi, typename T>
 __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v)[16], const uint32_t (&lo)[8],
-                                               const TgParams& p, const TgTask& k, int c, int m, int lane) {
+                                               const TgParams& p, const TgTask& k, int c, int m, int lane, long long low_at) {
   const int row0 = k.n0 + c * 32, nrow = k.cols - c * 32, mcol = p.M - m;
   if (Epi == kTgUpdate && mcol > 0 && nrow > 0) {
-    uint4* at = reinterpret_cast<uint4*>(p.lo_out + tg_low_at(p, k, c, m, lane));
+    uint4* at = reinterpret_cast<uint4*>(p.lo_out + low_at);
     at[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     at[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
   }
@@ -912,8 +921,10 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
     const float ca = kWide ? f.ca * alpha : f.ca, cb = kWide ? f.cb * alpha : f.cb * alpha * alpha;
     const bool low = kWide && f.lo_in != nullptr && m < p.M;
     uint4 l0 = make_uint4(0, 0, 0, 0), l1 = l0;
+    long long low_at = kWide ? tg_low_at(p, k, part, m, lane) : 0;
+    const long long low_step = kWide ? (p.ldi >> 5) * (1024 * kParts) : 0;
     if (low && part * 32 < k.nt) {
-      const uint4* from = reinterpret_cast<const uint4*>(f.lo_in + tg_low_at(p, k, part, m, lane));
+      const uint4* from = reinterpret_cast<const uint4*>(f.lo_in + low_at);
       l0 = __ldcg(from);
       l1 = __ldcg(from + 1);
     }
@@ -942,7 +953,7 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
       }
       uint32_t v[16], lo[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
       if (low && again) {
-        const uint4* low_from = reinterpret_cast<const uint4*>(f.lo_in + tg_low_at(p, k, c + kParts, m, lane));
+        const uint4* low_from = reinterpret_cast<const uint4*>(f.lo_in + low_at + low_step);
         l0 = __ldcg(low_from);
         l1 = __ldcg(low_from + 1);
       }
@@ -962,7 +973,8 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + at.acc * 8);
       }
-      tg_piece_store<Mode, Epi, T>(slot, v, lo, p, k, c, m, lane);
+      tg_piece_store<Mode, Epi, T>(slot, v, lo, p, k, c, m, lane, low_at);
+      low_at += low_step;
       if (reads) slot += kTgPiece;
     }
     if (any) {
