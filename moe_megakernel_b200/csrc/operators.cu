@@ -570,7 +570,10 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
 
   OrthoParams o{G, ldg, bsg, m, n, xs, eps, reinterpret_cast<double*>(ws + L.partial),
                 reinterpret_cast<float*>(ws + L.alpha), reinterpret_cast<__half*>(ws + L.x[0]), ws + L.lo, L.ldx, L.bsx,
-                L.bsl, (int)std::min<long long>(kOrthoChunks, ((long long)m * n + 4095) / 4096)};
+                L.bsl, 0};
+  // blocks of 4096 entries or more, some sixteen to an SM over the batch
+  o.chunks = (int)std::min<long long>({(long long)kOrthoChunks, ((long long)m * n + 4095) / 4096,
+                                       std::max(1ll, (16ll * sms + batch - 1) / batch)});
   const bool fp32 = dtype == MOE_DTYPE_FP32;
   const dim3 grid(o.chunks, batch);
   if (int rc = launch_pass(fp32 ? moe_ortho_norm_kernel<float> : moe_ortho_norm_kernel<bf16>, grid, o, st)) return rc;
