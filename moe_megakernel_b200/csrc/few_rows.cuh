@@ -8,7 +8,9 @@
 // distributed shared memory: every CTA leaves its fp32 tile in its own shared
 // memory, and after a cluster barrier adds up its 1/S of the entries over the
 // peers, in rank order, so a result does not depend on timing and no workspace
-// or counter is needed.
+// or counter is needed. Bound by HBM and by the 4 to 5 us of set-up, first load
+// and join: one row of 14336 -> 4096 features 22 us (117 MB, 5.3 TB/s), 37 rows
+// 26 us, 4096 -> 4096 10.5 us; without the split 60 and 21 us.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"

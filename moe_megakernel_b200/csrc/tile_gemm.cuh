@@ -19,9 +19,19 @@
 // own shared memory; both CTAs' bytes are counted on the leader's barrier.
 // Two TMEM accumulators let a tile's epilogue run under the next tile's MMAs.
 // Tiles are dealt round robin; nothing is exchanged between pairs. Warp 3 works
-// out each tile (up to six integer divisions, about 1200 cycles) up to four tiles ahead of the
-// others: in every role's own path this cost 2 us a tile, more than the MMAs of
-// a 256-row weight gradient.
+// out each tile (up to six integer divisions, about 1200 cycles) up to four tiles
+// ahead of the others, so that no role spends its own time on it.
+//
+// What bounds it: a k block (64 k) of a 256 x 256 tile is 512 cycles of MMA by
+// the nominal rate (474 measured with its operands at hand) and 32 KB of loads in
+// each CTA, 64 bytes a cycle and SM, which is what L2 delivers: with operands
+// shared by few pairs at a time a k block takes 600 to 750 cycles. 8192 x 4096 ->
+// 14336 features, bf16: 609 us (1.58 PFLOP/s) in a burst and 718 us (1.34) under
+// the 1 kW cap, where the clock settles near 1.2 GHz; the library's plain product
+// of the same matrices 628 and 716 us on the same box. Tensor pipe busy 85 to 89 %
+// of the cycles (dense 4096 x 4096 -> 14336 and 128 uneven groups, ncu). Tiles of
+// 256 columns are the largest with two accumulators in TMEM; smaller ones load
+// more a FLOP (see pick_tile in operators.cu).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -440,9 +450,10 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, TgState& at, uint8_t*
 
 // ---------------------------------------------------------------- MMA (leader)
 // The warp runs the loop together and one lane issues: the descriptors are then
-// warp-uniform values. With the loop inside a one-lane branch an MMA took 70
-// cycles to issue, more than its share of the tensor core's time (64 at 256
-// columns and two CTAs' operands).
+// warp-uniform values. With the loop inside a one-lane branch a k block took some
+// 550 cycles to issue whatever its columns (an MMA 75, the barriers 250), which
+// held narrow tiles back most: 256 rows over 163 experts of 7168 x 2048 took
+// 955 us instead of 729, 37 rows of 14336 -> 4096 109 us instead of 61.
 template <int Mode, bool PMn, bool QMn>
 __device__ void tg_mma(const TgParams& p, TgSmem& s, TgState& at, uint32_t tiles, uint32_t tmem) {
   const uint32_t fmt = p.f16 ? 0u : 1u;
