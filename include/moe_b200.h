@@ -557,9 +557,9 @@ size_t moe_linear_backward_workspace_bytes(int T, int N, int activation, int bia
  * (X^T X on the right when m > n), with the step's a, b, c from the HOST array
  * coeffs [steps, 3]; out bf16 [m, n] (pitches ldo, bso) receives the last X.
  * X is carried to 19 bits (an fp16 value and 8 bits more); A, bA + cAA and X
- * enter the tensor-core products as fp16, accumulated in fp32; A and bA + cAA are stored
- * times 1024, so their entries must stay below 64 in magnitude (with the usual
- * quintic coefficients they stay below 7). A gradient of zeros gives zeros; an
+ * enter the tensor-core products as fp16, accumulated in fp32. A and bA + cAA
+ * (less a multiple of the identity) are stored times 1024, so their entries must
+ * stay below 32 in magnitude (with the usual quintic coefficients below 7). A gradient of zeros gives zeros; an
  * infinity or NaN in a matrix makes that matrix's output NaN and no other's.
  * 1 <= steps <= 64; m, n <= 65536; batch <= 65535. workspace: 256-byte aligned,
  * moe_orthogonalize_workspace_bytes(batch, m, n). */

@@ -198,16 +198,17 @@ int pick_tile(long long rows, int mt, int batch, int pairs, bool q_mn) {
   return best;
 }
 
-// N tile of a ragged product: twice the mean rows of a group, so that most
-// groups are one tile and the stages of a launch with few rows are small; and
-// less where the tiles would leave pairs idle (taking every group to end in half
-// a tile, with the costs of pick_tile).
+// Largest N tile of a ragged product (a group of fewer rows takes fewer columns
+// anyway): 256, and less where the tiles would leave pairs idle, taking every
+// group to end in half a tile, with the costs of pick_tile. A smaller limit for
+// small groups makes no difference to their time (1 to 64 rows in each of 128
+// experts of 2048 x 2048 or 768: within 2 % at 32, 64, 128 and 256, and 6 %
+// slower at 32 for 16 and 32 rows) and costs a large group among them its reuse
+// (1500 rows among experts of 4: 84 us at 32, 77 at 256).
 int ragged_tile(int rows, int groups, int mt, int pairs) {
-  const int mean = (rows + groups - 1) / groups;
-  const int most = mean <= 16 ? 32 : mean <= 32 ? 64 : mean <= 64 ? 128 : 256;
-  int best = most;
+  int best = 256;
   long long least = -1;
-  for (int nt = most; nt >= 32; nt /= 2) {
+  for (int nt = 256; nt >= 32; nt /= 2) {
     const long long tiles = ((long long)rows / nt + (groups + 1) / 2) * mt;
     const long long cost = (tiles + pairs - 1) / pairs * (256 + nt);
     if (least < 0 || cost < least) {
@@ -546,7 +547,8 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
       !(eps >= 0.f) || !aligned(error_word, 4))
     return MOE_ERR_INVALID_ARG;
   if (steps < 1 || steps > 64 || std::max(m, n) > (1 << 16) || batch > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (ldg < n || ldo < n || (batch > 1 && (bsg < ldg * (m - 1) + n || bso < ldo * (m - 1) + n)))
+  constexpr long long kMost = 1ll << 40;   // pitches, so that their products stay in 64 bits
+  if (ldg < n || ldo < n || ldg > kMost || ldo > kMost || (batch > 1 && (bsg < ldg * (m - 1) + n || bso < ldo * (m - 1) + n)))
     return MOE_ERR_INVALID_ARG;
   if (batch > 0 && (G == nullptr || out == nullptr || !aligned(G, elem) || !aligned(out, 2))) return MOE_ERR_INVALID_ARG;
   const OrthoLayout L = ortho_layout(std::max(batch, 1), m, n);

@@ -86,7 +86,7 @@ ORTHO = dict(G=A, ldg=40, bsg=40 * 30, batch=2, m=30, n=40, dtype=0, steps=1, co
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(G=None), 1), (dict(out=None), 1), (dict(G=ctypes.c_void_p((1 << 20) + 1)), 1), (dict(ldg=39), 1),
+    (dict(G=None), 1), (dict(out=None), 1), (dict(ldg=1 << 50), 1), (dict(G=ctypes.c_void_p((1 << 20) + 1)), 1), (dict(ldg=39), 1),
     (dict(ldo=8), 1), (dict(bsg=100), 1), (dict(bso=100), 1), (dict(batch=-1), 1), (dict(m=0), 1), (dict(dtype=1), 1),
     (dict(coeffs=None), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(steps=0), 2), (dict(steps=65), 2),
     (dict(m=70000, ldg=70000, bsg=1 << 40), 2), (dict(workspace=None), 1), (dict(workspace=ODD), 1),
