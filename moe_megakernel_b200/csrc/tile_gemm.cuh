@@ -48,6 +48,7 @@ constexpr int kTgThreads = 384;
 constexpr int kTgEpiWarps = 8;
 constexpr int kTgMaxStages = 12;
 constexpr int kTgMaxGroups = 1024;
+constexpr int kTgSorted = 256;           // groups that a weight gradient sorts by size
 constexpr int kTgRing = 4;               // tiles worked out ahead
 constexpr int kTgABytes = 128 * 128;     // 128 rows of P, 64 k each
 constexpr long long kTgTimeoutCycles = 4000000000ll;   // about two seconds
@@ -130,10 +131,12 @@ struct TgSmem {
   int abort;
   int total;
   // behind it, in ragged products: start[groups] and count[groups], the groups' rows as used (an
-  // invalid group is empty), and tile0[groups + 1], the first N tile of each group (ragged N)
+  // invalid group is empty), and tile0[groups + 1], the first N tile of each group (ragged N), or
+  // order[groups], the groups from the largest to the smallest (ragged K)
   __device__ int* start() { return reinterpret_cast<int*>(this + 1); }
   __device__ int* count(int groups) { return start() + groups; }
   __device__ int* tile0(int groups) { return start() + 2 * groups; }
+  __device__ int* order(int groups) { return start() + 2 * groups; }
 };
 
 constexpr int kTgSmemMax = 232448;   // shared memory of a CTA
@@ -246,6 +249,7 @@ __device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, TgSmem& s)
     tg_split(p.N, p.nt, n, k.n0, k.cols);
     k.m0 = m << 8;
     if (Mode == kTgRaggedK) {
+      k.g = s.order(p.groups)[k.g];
       k.k0 = s.start()[k.g];
       k.klen = s.count(p.groups)[k.g];
     } else {
@@ -306,7 +310,8 @@ struct TgState {
 
 template <int Mode>
 __device__ void tg_schedule(const TgParams& p, TgSmem& s, TgState& at, int first, int end, int step) {
-  for (int t = first;; t += step) {
+  int t = first;
+  for (int round = 0;; ++round) {
     TgTask k{};
     k.g = -1;
     if (t < end) k = tg_decode<Mode>(t, p, s);
@@ -318,6 +323,8 @@ __device__ void tg_schedule(const TgParams& p, TgSmem& s, TgState& at, int first
     __syncwarp();
     at.list.step();
     if (k.g < 0) return;
+    // round robin; tiles sorted by their time (ragged K) in turn from either end
+    t = Mode == kTgRaggedK && (round & 1) == 0 ? (round + 1) * step + step - 1 - first : (round + 1) * step + first;
   }
 }
 
@@ -1083,6 +1090,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
     }
   }
   __syncthreads();
+  if (Mode == kTgRaggedK) {
+    // The time of a tile goes with its group's rows, and all tiles of a group take the same: dealt from
+    // the largest group to the smallest, forwards and backwards in turn, the pairs' shares differ less
+    // (128 groups of 100 to 6000 rows: 6 % of the mean instead of 15 %). Ranks by counting, so only for
+    // some hundred groups.
+    const int* count = s.count(p.groups);
+    int* order = s.order(p.groups);
+    for (int e = threadIdx.x; e < p.groups; e += kTgThreads) {
+      int rank_of = e;
+      if (p.groups <= kTgSorted) {
+        rank_of = 0;
+        for (int f = 0; f < p.groups; ++f) rank_of += count[f] > count[e] || (count[f] == count[e] && f < e) ? 1 : 0;
+      }
+      order[rank_of] = e;
+    }
+  }
   if (Mode == kTgRaggedN) {
     if (warp == 0) {
       const int* count = s.count(p.groups);
