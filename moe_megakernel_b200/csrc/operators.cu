@@ -219,15 +219,18 @@ int ragged_tile(int rows, int groups, int mt, int pairs) {
   return best;
 }
 
-template <bool PMn>
-int launch_rows(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
-  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedN, PMn, false, kTgStore, __half>(p, tiles, st)
-                                 : launch<kTgRaggedN, PMn, false, kTgStore, bf16>(p, tiles, st);
+// Forward products have the layer's epilogue; gradients (a transposed W, a weight gradient) store what they are.
+int launch_rows(TgParams& p, bool transpose, int dtype, long long tiles, cudaStream_t st) {
+  if (dtype == MOE_DTYPE_FP16)
+    return transpose ? launch<kTgRaggedN, false, false, kTgPlain, __half>(p, tiles, st)
+                     : launch<kTgRaggedN, true, false, kTgStore, __half>(p, tiles, st);
+  return transpose ? launch<kTgRaggedN, false, false, kTgPlain, bf16>(p, tiles, st)
+                   : launch<kTgRaggedN, true, false, kTgStore, bf16>(p, tiles, st);
 }
 
 int launch_wgrad(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
-  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedK, true, true, kTgStore, __half>(p, tiles, st)
-                                 : launch<kTgRaggedK, true, true, kTgStore, bf16>(p, tiles, st);
+  return dtype == MOE_DTYPE_FP16 ? launch<kTgRaggedK, true, true, kTgPlain, __half>(p, tiles, st)
+                                 : launch<kTgRaggedK, true, true, kTgPlain, bf16>(p, tiles, st);
 }
 
 // The cut of a few-rows product (few_rows.cuh) and its time in microseconds, and
@@ -341,7 +344,7 @@ int rows_product(TgParams& p, const void* x, long long ldx, const void* W, int r
     }
   }
   if (!set_maps(p, P, !transpose, Q, false) || !set_out(p, y, N, rows, ldy, 1, 0)) return MOE_ERR_CUDA;
-  return transpose ? launch_rows<false>(p, dtype, tiles, st) : launch_rows<true>(p, dtype, tiles, st);
+  return launch_rows(p, transpose, dtype, tiles, st);
 }
 
 // dW[g] = x_g^T dy_g

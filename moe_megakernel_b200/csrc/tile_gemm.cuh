@@ -66,6 +66,7 @@ enum TgEpilogue : int {
   kTgPoly = 2,      // B = b A + c A A
   kTgUpdate = 3,    // X' = a X + B X (X as a pair of fp16 values)
   kTgUpdateOut = 4, // the same, stored as bf16 at the caller's place
+  kTgPlain = 5,     // the accumulator alone (gradients)
 };
 
 enum TgAct : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
@@ -677,14 +678,17 @@ __device__ __forceinline__ void tg_piece_in(uint32_t piece, const void* g, long 
 }
 // A piece as one TMA store (its place order is the 64-byte swizzle), clipped at
 // the tensor's ends. The piece's shared memory is in use until tg_bulk_read.
+__device__ __forceinline__ void tg_bulk_store(uint32_t piece, const CUtensorMap* m, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(piece), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 __device__ __forceinline__ void tg_piece_bulk(uint32_t piece, const CUtensorMap* m, int c0, int c1, int c2, int lane) {
   ptx::fence_proxy_async_shared();
   __syncwarp();
   if (lane == 0) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(piece), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
+    tg_bulk_store(piece, m, c0, c1, c2);
     ptx::bulk_commit();
   }
 }
@@ -716,7 +720,9 @@ __device__ __forceinline__ void tg_pack(const uint32_t (&r)[2][16], uint32_t (&v
 // epilogue reads, so that a tile's whole input is on its way before its MMAs end
 // (with two, the wait for each third and fourth piece took longer than the piece).
 template <int Epi>
-__host__ __device__ constexpr int tg_slots(bool residual) { return Epi == kTgGram || (Epi == kTgStore && !residual) ? 1 : 4; }
+__host__ __device__ constexpr int tg_slots(bool residual) {
+  return Epi == kTgPlain ? 2 : Epi == kTgGram || (Epi == kTgStore && !residual) ? 1 : 4;
+}
 template <int Epi>
 __host__ __device__ constexpr int tg_epi_bytes(bool residual) { return kTgEpiWarps * kTgPiece * tg_slots<Epi>(residual); }
 
@@ -900,6 +906,88 @@ __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v
   }
 }
 
+// The accumulator alone, two pieces at a time: half as many waits and fences,
+// which weigh as much as the stores where a tile's reduction is short (a weight
+// gradient of 256 rows has four k blocks and writes 128 KB): 32768 rows in 128
+// uneven groups of 2048 x 768 182 us instead of 188, of which writing 403 MB is
+// 104 by itself.
+template <int Mode, typename T>
+__device__ void tg_epilogue_plain(const TgParams& p, TgSmem& s, TgState& at, uint32_t store, uint32_t tmem, uint32_t rank,
+                                  int warp) {
+  constexpr int kParts = kTgEpiWarps / 4;
+  const int lane = ptx::lane_id();
+  const int quad = warp & 3, part = (warp - 4) >> 2;
+  const uint32_t leader_empty0 = ptx::mapa(ptx::smem_u32(&s.acc_empty[0]), 0);
+  const uint32_t slot = store + (warp - 4) * 2 * kTgPiece;
+  TgTask k, next;
+  bool more = at.list.next(k, p, s);
+  while (more) {
+    const bool any = k.klen > 0;
+    const int m = k.m0 + (int)rank * 128 + quad * 32;
+    const uint32_t from = tmem + at.acc * 256 + ((uint32_t)(quad * 32) << 16);
+    uint32_t r[2][2][16];   // [piece]
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if ((2 * c + h) * 32 < k.nt) {
+          tg_tmem_frag(from + (2 * c + h) * 32, r[h][0]);
+          tg_tmem_frag(from + (2 * c + h) * 32 + (16u << 16), r[h][1]);
+        }
+    };
+    if (any) {
+      if (!tg_wait_warp(&s.acc_full[at.acc], at.acc_phase, p, s)) break;
+      ptx::tc_fence_after();
+      fetch(part);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) r[i >> 5][(i >> 4) & 1][i & 15] = 0;
+    }
+    more = at.list.next(next, p, s);
+#pragma unroll 1
+    for (int c = part; c * 64 < k.nt; c += kParts) {
+      const bool again = (c + kParts) * 64 < k.nt;
+      if (any) ptx::tmem_ld_wait();
+      uint32_t v[2][16];
+      tg_pack<T>(r[0], v[0]);
+      tg_pack<T>(r[1], v[1]);
+      if (any) {
+        if (again) {
+          fetch(c + kParts);
+        } else {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_peer(leader_empty0 + at.acc * 8);
+        }
+      }
+      if (m >= p.M) continue;
+      tg_bulk_read(lane);
+      tg_piece_put<kRowsN>(slot, v[0], lane);
+      tg_piece_put<kRowsN>(slot + kTgPiece, v[1], lane);
+      ptx::fence_proxy_async_shared();
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row0 = k.n0 + (2 * c + h) * 32, nrow = k.cols - (2 * c + h) * 32;
+        if (nrow <= 0) break;
+        if (Mode == kTgRaggedN && nrow < 32 && row0 + nrow != p.N)   // the group ends inside the piece
+          tg_piece_out(slot + h * kTgPiece, reinterpret_cast<T*>(p.out) + (long long)row0 * p.ldo + m, p.ldo, nrow,
+                       p.M - m, lane);
+        else if (lane == 0)
+          tg_bulk_store(slot + h * kTgPiece, &p.tm_out, m, row0, Mode == kTgRaggedN ? 0 : k.g);
+      }
+      if (lane == 0) ptx::bulk_commit();
+      __syncwarp();
+    }
+    if (any) {
+      if (part * 64 >= k.nt && lane == 0) ptx::mbar_arrive_peer(leader_empty0 + at.acc * 8);
+      at.next_acc();
+    }
+    k = next;
+  }
+  if (lane == 0) ptx::bulk_wait_all();
+  __syncwarp();
+}
+
 // The accumulator of the next piece (and its low bits of X) is on its way while
 // a piece is stored, and the accumulator buffer is given back before the last
 // piece is.
@@ -1054,7 +1142,8 @@ __device__ __forceinline__ void tg_product(const TgParams& p, const TgFactors& f
   } else if (warp == 3) {
     tg_schedule<Mode>(p, s, at, first, end, step);
   } else {
-    tg_epilogue<Mode, Epi, T>(p, f, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
+    if (Epi == kTgPlain) tg_epilogue_plain<Mode, T>(p, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
+    else tg_epilogue<Mode, Epi, T>(p, f, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
   }
   __syncwarp();
 }
