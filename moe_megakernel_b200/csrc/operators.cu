@@ -233,29 +233,42 @@ int launch_wgrad(TgParams& p, int dtype, long long tiles, cudaStream_t st) {
                                  : launch<kTgRaggedK, true, true, kTgPlain, bf16>(p, tiles, st);
 }
 
-// The cut of a few-rows product (few_rows.cuh) and its time in microseconds, and
-// the time of the same product on CTA pairs (tile_gemm.cuh). The figures are
-// fits to measured times of 8 to 120 MB of weights at 1 to 512 rows: a k block
-// (64 k of 128 features) takes a CTA 0.6 us when two run on every SM and W comes
-// from HBM, and a CTA 4.5 us besides (set-up, first load, joining the parts),
-// with 7 us more by 128 rows; a pair takes 0.27 us a k block of up to 240 columns
-// (its weight tile is 256 features) and 3 us besides, but its reduction is not
-// split. Measured, few rows / pairs: 14336 -> 4096 features, 37 rows 25 / 61 us;
-// 4096 -> 14336 24 / 24 us; 2048 -> 40000 43 / 36 us; 8192 -> 1024, 256 rows 17 / 37 us.
+// The cut of a product of few tiles (few_rows.cuh) and its time in microseconds,
+// and the time of the same product as whole reductions on CTA pairs
+// (tile_gemm.cuh). The figures are fits to measured times of 8 to 160 MB of
+// weights at 1 to 768 rows. Single CTAs: a k block (64 k of 128 features) 0.6 us
+// when two run on every SM and W comes from HBM, less with fewer down to 0.3, and
+// 4.5 us besides (set-up, first load, join), with 7 us more by 128 rows. Pairs: 0.27 us a k block of up to
+// 240 columns of a 256-feature tile, and 3 us besides for whole reductions, 5.5
+// and 3 more by 128 columns for split ones. Measured, split (the kind taken) /
+// whole: 14336 -> 4096 features, 37 rows 25 (single) / 61 us; 4096 -> 14336 24 / 24;
+// 2048 -> 40000 43 / 36.
 struct FewCut {
   int nt, split;
+  bool pair;
   double us;
 };
 FewCut few_cut(int T, int M, int K, int sms, bool q_mn) {
-  FewCut best{T <= 32 && !q_mn ? 32 : T <= 64 ? 64 : 128, 1, 1e30};   // an MN-major Q comes in boxes of 64
-  const int across = (T + best.nt - 1) / best.nt;
+  const int nt = T <= 32 && !q_mn ? 32 : T <= 64 ? 64 : 128;   // an MN-major Q comes in boxes of 64
+  FewCut best{nt, 1, false, 1e30};
+  const int nk = (K + 63) / 64;
+  const int across = (T + nt - 1) / nt;
   if (across > 65535) return best;   // the grid's second extent
   const long long cells = (long long)((M + 127) / 128) * across;
-  const int nk = (K + 63) / 64;
   for (int c = 1; c <= kFewMaxSplit && c <= std::max(1, nk / 2); ++c) {
     const double rounds = (double)((cells * c + 2 * sms - 1) / (2 * sms));
-    const double us = rounds * ((nk + c - 1) / c * 0.6 + 4.5 + 7.0 * std::min(T, 128) / 128);
+    const double block = std::max(0.3, 0.6 * std::min(1.0, (double)(cells * c) / (2 * sms)));
+    const double us = rounds * ((nk + c - 1) / c * block + 4.5 + 7.0 * std::min(T, 128) / 128);
     if (us < best.us) best.split = c, best.us = us;
+  }
+  const int wide = (T + 255) / 256, unit = q_mn ? 128 : 32;
+  const int each = ((T + wide - 1) / wide + unit - 1) / unit * unit;
+  const long long pair_cells = (long long)((M + 255) / 256) * wide;
+  for (int c = 2; 2 * c <= kFewMaxSplit && c <= nk / 2; ++c) {
+    const int at_once = c == 2 ? sms / 4 - 1 : c == 3 ? sms / 7 : sms / 12;   // clusters: large ones leave SMs of a GPC over
+    const double rounds = (double)((pair_cells + at_once - 1) / std::max(1, at_once));
+    const double us = rounds * ((nk + c - 1) / c * std::max(0.27, each * 0.0011) + 5.5 + 3.0 * each / 128);
+    if (us < best.us) best = FewCut{each, c, true, us};
   }
   return best;
 }
@@ -263,15 +276,16 @@ double pairs_us(long long tiles, int nt, int K, int pairs) {
   return (double)((tiles + pairs - 1) / pairs) * ((K + 63) / 64 * std::max(0.27, nt * 0.0011) + 3.0);
 }
 
-template <bool PMn, bool QMn, typename T>
-int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Operand& Q, cudaStream_t st) {
+template <bool PMn, bool QMn, bool Pair, typename T>
+int launch_few_kind(const TgParams& p, const FewCut& cut, const Operand& P, const Operand& Q, cudaStream_t st) {
   static std::atomic<int> ready[kMaxDevices];
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return MOE_ERR_CUDA;
-  auto kernel = moe_few_rows_kernel<PMn, QMn, T>;
+  auto kernel = moe_few_rows_kernel<PMn, QMn, Pair, T>;
+  constexpr int most = Pair ? kFewSmemTilesPair : kFewSmemTiles;
   if (!ready[d].load()) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kFewSmemTiles + 1024 + sizeof(FewSmem))) != cudaSuccess)
+                             (int)(most + 1024 + sizeof(FewSmem))) != cudaSuccess)
       return MOE_ERR_CUDA;
     ready[d].store(1);
   }
@@ -281,7 +295,8 @@ int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Ope
   f.T = p.N;
   f.nt = cut.nt;
   f.split = cut.split;
-  f.stages = std::min(kFewMaxStages, kFewSmemTiles / few_stage_bytes(f.nt));
+  const int cols = Pair ? f.nt / 2 : f.nt;
+  f.stages = std::min(kFewMaxStages, most / few_stage_bytes(cols));
   f.f16 = p.f16;
   f.err = p.err;
   f.out = p.out;
@@ -292,21 +307,29 @@ int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Ope
   f.z = p.z;
   f.ldz = p.ldz;
   f.act = p.act;
-  if (!map3(&f.tm_w, P, PMn ? 64 : 128, p.f16 != 0) || !map3(&f.tm_x, Q, QMn ? 64 : f.nt, p.f16 != 0)) return MOE_ERR_CUDA;
+  if (!map3(&f.tm_w, P, PMn ? 64 : 128, p.f16 != 0) || !map3(&f.tm_x, Q, QMn ? 64 : cols, p.f16 != 0)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = f.split;
+  const int ctas = f.split * (Pair ? 2 : 1);
+  at[1].val.clusterDim.x = ctas;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = f.split > 1 ? 2 : 1;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   cfg.blockDim = dim3(kFewThreads);
-  cfg.gridDim = dim3((p.M + 127) / 128 * f.split, (p.N + f.nt - 1) / f.nt);
-  cfg.dynamicSmemBytes = few_smem_bytes(f.nt, f.stages);
+  const int features = Pair ? 256 : 128;
+  cfg.gridDim = dim3((p.M + features - 1) / features * ctas, (p.N + f.nt - 1) / f.nt);
+  cfg.dynamicSmemBytes = few_smem_bytes(cols, f.stages);
   cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, kernel, f) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <bool PMn, bool QMn, typename T>
+int launch_few(const TgParams& p, const FewCut& cut, const Operand& P, const Operand& Q, cudaStream_t st) {
+  return cut.pair ? launch_few_kind<PMn, QMn, true, T>(p, cut, P, Q, st)
+                  : launch_few_kind<PMn, QMn, false, T>(p, cut, P, Q, st);
 }
 
 // y = x W (transpose: x W^T) for one or several row groups; epilogue fields of p set by the caller.

@@ -217,7 +217,8 @@ def slope64(z, act):
     (129, 8, 8, "relu", True, True, True), (300, 584, 776, "silu", True, True, False),
     (37, 8192, 264, "gelu", True, True, True), (200, 4096, 512, "silu", True, True, True),
     (500, 6000, 136, None, True, True, True), (31, 320, 40000, "relu", True, False, False),
-    (2100, 136, 1288, "gelu", True, True, True),
+    (2100, 136, 1288, "gelu", True, True, True), (384, 6000, 2056, "silu", True, True, True),
+    (512, 2048, 1000, None, False, True, False), (700, 3000, 264, "gelu", True, False, True),
     (1031, 256, 520, "gelu", True, False, True)])
 def test_linear(T, K, N, act, bias, res, save, dtype):
     x, W = rand(T, K, seed=21, dtype=dtype), rand(K, N, seed=22, dtype=dtype, std=K ** -0.5)
@@ -261,7 +262,8 @@ def test_linear_onto_the_residual_itself_and_strided_rows():
     (1, 64, 128, "silu", True), (5, 8, 8, None, True), (37, 520, 264, "gelu", True), (128, 136, 1032, "relu", False),
     (200, 256, 256, "gelu_tanh", True), (1031, 328, 520, "silu", True), (4100, 64, 72, None, True),
     (64, 256, 4096, "gelu", True), (150, 520, 6000, "silu", False), (3812, 104, 776, None, False),
-    (1598, 664, 256, "silu", True), (2051, 24, 136, "relu", True), (777, 200, 96, "gelu", False)])
+    (1598, 664, 256, "silu", True), (2051, 24, 136, "relu", True), (777, 200, 96, "gelu", False), (5000, 300 * 2, 520, "silu", True),
+    (384, 1000, 6000, "gelu", True)])
 def test_linear_backward(T, K, N, act, bias, dtype):
     x, W = rand(T, K, seed=41, dtype=dtype), rand(K, N, seed=42, dtype=dtype, std=K ** -0.5)
     dy = rand(T, N, seed=43, dtype=dtype, std=0.2)
