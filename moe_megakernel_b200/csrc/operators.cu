@@ -415,12 +415,12 @@ struct OrthoLayout {
 };
 OrthoLayout ortho_layout(int batch, int m, int n) {
   OrthoLayout L{};
-  const int p = std::min(m, n);
-  L.ldx = (long long)up(n, 64);
+  const int p = std::min(m, n);   // X is kept with the long side contiguous
+  L.ldx = (long long)up(std::max(m, n), 64);
   L.lda = (long long)up(p, 64);
-  L.bsx = L.ldx * m;
+  L.bsx = L.ldx * p;
   L.bsa = L.lda * p;
-  L.bsl = L.ldx * (long long)up(m, 32);
+  L.bsl = L.ldx * (long long)up(p, 32);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -596,16 +596,21 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
   while ((1ll << (2 * (s + 1))) <= q0) ++s;
   const float xs = (float)(1 << s), as = 1024.f;   // A and B are stored times 2^10
 
-  OrthoParams o{G, ldg, bsg, m, n, xs, eps, reinterpret_cast<double*>(ws + L.partial),
-                reinterpret_cast<float*>(ws + L.alpha), reinterpret_cast<__half*>(ws + L.x[0]), ws + L.lo, L.ldx, L.bsx,
+  const bool fp32 = dtype == MOE_DTYPE_FP32;
+  OrthoParams o{G, ldg, bsg, m, n, tall ? 1 : 0, xs, eps, reinterpret_cast<double*>(ws + L.partial),
+                reinterpret_cast<float*>(ws + L.alpha), reinterpret_cast<__half*>(ws + L.x[0]),
+                fp32 ? ws + L.lo : nullptr, L.ldx, L.bsx,
                 L.bsl, 0};
   // blocks of 4096 entries or more, some sixteen to an SM over the batch
   o.chunks = (int)std::min<long long>({(long long)kOrthoChunks, ((long long)m * n + 4095) / 4096,
                                        std::max(1ll, (16ll * sms + batch - 1) / batch)});
-  const bool fp32 = dtype == MOE_DTYPE_FP32;
   const dim3 grid(o.chunks, batch);
   if (int rc = launch_pass(fp32 ? moe_ortho_norm_kernel<float> : moe_ortho_norm_kernel<bf16>, grid, o, st)) return rc;
-  if (int rc = launch_pass(fp32 ? moe_ortho_scale_fp32_kernel : moe_ortho_scale_bf16_kernel, grid, o, st)) return rc;
+  if (int rc = launch_pass(fp32 ? moe_ortho_scale_pieces_kernel<float>
+                           : tall ? moe_ortho_scale_pieces_kernel<bf16>
+                                  : moe_ortho_scale_bf16_kernel,
+                           grid, o, st))
+    return rc;
 
   const Operand A{ws + L.a, (uint64_t)p0, (uint64_t)p0, (uint64_t)L.lda, (uint64_t)batch, (uint64_t)L.bsa};
   const Operand B{ws + L.b, (uint64_t)p0, (uint64_t)p0, (uint64_t)L.lda, (uint64_t)batch, (uint64_t)L.bsa};
@@ -613,16 +618,19 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
   base.err = error_word;
   base.f16 = 1;
   base.groups = batch;
-  // A = X X^T (X^T X for a tall X), from X in buffer k
+  auto operand_x = [&](int k) {
+    return Operand{ws + L.x[k], (uint64_t)q0, (uint64_t)p0, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
+  };
+  // A = X X^T, from X in buffer k
   auto gram = [&](int k, TgParams& g) {
-    const Operand X{ws + L.x[k], (uint64_t)n, (uint64_t)m, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
+    const Operand X = operand_x(k);
     g = base;
     g.M = g.N = p0;
     g.K = q0;
     g.nt = 256;
     g.factors.cb = as / (xs * xs);
     g.backwards = 1;   // from the batches that the step before wrote last, which L2 still holds
-    return set_maps(g, X, tall, X, tall) && set_out(g, ws + L.a, p0, p0, L.lda, batch, L.bsa);
+    return set_maps(g, X, false, X, false) && set_out(g, ws + L.a, p0, p0, L.lda, batch, L.bsa);
   };
   // B = b A + c A A
   auto poly = [&](TgParams& g) {
@@ -634,15 +642,14 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g.in_bs = L.bsa;
     return set_maps(g, A, false, A, false) && set_out(g, ws + L.b, p0, p0, L.lda, batch, L.bsa);
   };
-  // X' = a X + B X, from buffer k to the other (last: to the caller); rows of X on the N side, columns on the M side:
-  // wide X'[r, c] = sum_k X[k, c] B[r, k], tall X'[r, c] = sum_k B[c, k] X[r, k] (B symmetric)
+  // X' = a X + B X, from buffer k to the other (last: to the caller, a tall matrix back in its own order):
+  // rows of X on the N side, columns on the M side, X'[r, c] = sum_k X[k, c] B[r, k]
   auto update = [&](int k, bool last, TgParams& g) {
-    const Operand X{ws + L.x[k], (uint64_t)n, (uint64_t)m, (uint64_t)L.ldx, (uint64_t)batch, (uint64_t)L.bsx};
+    const Operand X = operand_x(k);
     g = base;
-    g.M = n;
-    g.N = m;
-    g.K = p0;
-    g.nt = pick_tile(m, (n + 255) / 256, batch, pairs, false);
+    g.M = q0;
+    g.N = g.K = p0;
+    g.nt = pick_tile(p0, (q0 + 255) / 256, batch, pairs, false);
     g.in = reinterpret_cast<const __half*>(ws + L.x[k]);
     g.lo_out = ws + L.lo;
     g.lo_bs = L.bsl;
@@ -652,24 +659,25 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
       g.out = out;
       g.ldo = ldo;
       g.out_bs = bso;
-    } else if (!set_out(g, ws + L.x[k ^ 1], n, m, L.ldx, batch, L.bsx)) {
+      g.transposed = tall ? 1 : 0;
+    } else if (!set_out(g, ws + L.x[k ^ 1], q0, p0, L.ldx, batch, L.bsx)) {
       return false;
     }
-    return tall ? set_maps(g, B, false, X, false) : set_maps(g, X, true, B, false);
+    return set_maps(g, X, true, B, false);
   };
   const uint8_t* lo_first = fp32 ? ws + L.lo : nullptr;   // a scaled bf16 gradient needs none
   // the symmetric products: half of the 256 x 256 tiles, stored twice; or, where these would leave most
   // pairs idle, all tiles of a width that fills them (with the costs of pick_tile)
   const int mt = (p0 + 255) / 256;
   const long long tri = (long long)batch * mt * (mt + 1) / 2;
-  const int all_nt = pick_tile(p0, mt, batch, pairs, tall);
+  const int all_nt = pick_tile(p0, mt, batch, pairs, false);
   const long long all = (long long)((p0 + all_nt - 1) / all_nt) * mt * batch;
   const bool half = (tri + pairs - 1) / pairs * (256 + 256) <= (all + pairs - 1) / pairs * (256 + all_nt);
   TgParams g1[2], g2, g3[2], g4;
   if (!gram(0, g1[0]) || !gram(1, g1[1]) || !poly(g2) || !update(0, false, g3[0]) || !update(1, false, g3[1]) ||
       !update((steps - 1) & 1, true, g4))
     return MOE_ERR_CUDA;
-  const long long tiles = (long long)((m + g4.nt - 1) / g4.nt) * ((n + 255) / 256) * batch;
+  const long long tiles = (long long)((p0 + g4.nt - 1) / g4.nt) * ((q0 + 255) / 256) * batch;
   if (tri >= (1ll << 30) || tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   // B is stored less a multiple d of the identity, X' = (a + d) X + (B - d I) X: once the singular values are
   // near 1, B's eigenvalues lie within a few tenths of b + c = -2.7, and the fp16 roundings of B and X enter X'
@@ -689,25 +697,19 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
     g2.factors = TgFactors{coeffs[3 * i + 1], coeffs[3 * i + 2] / as, nullptr, nullptr, -d * as};
     int rc;
     if (half) {
-      rc = tall ? launch<kTgSymmetric, true, true, kTgGram, __half>(a, tri, st)
-                : launch<kTgSymmetric, false, false, kTgGram, __half>(a, tri, st);
+      rc = launch<kTgSymmetric, false, false, kTgGram, __half>(a, tri, st);
       if (rc == MOE_OK) rc = launch<kTgSymmetric, false, false, kTgPoly, __half>(g2, tri, st);
     } else {
       a.nt = g2.nt = all_nt;
-      rc = tall ? launch<kTgBatched, true, true, kTgGram, __half>(a, all, st)
-                : launch<kTgBatched, false, false, kTgGram, __half>(a, all, st);
+      rc = launch<kTgBatched, false, false, kTgGram, __half>(a, all, st);
       if (rc == MOE_OK) rc = launch<kTgBatched, false, false, kTgPoly, __half>(g2, all, st);
     }
     if (rc) return rc;
     TgParams& x = last ? g4 : g3[i & 1];
     const float back = last ? 1.f / xs : 1.f;
     x.factors = TgFactors{(coeffs[3 * i] + d) * back, back / as, alpha, i == 0 ? lo_first : ws + L.lo, 0.f};
-    if (tall)
-      rc = last ? launch<kTgBatched, false, false, kTgUpdateOut, __half>(x, tiles, st)
-                : launch<kTgBatched, false, false, kTgUpdate, __half>(x, tiles, st);
-    else
-      rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(x, tiles, st)
-                : launch<kTgBatched, true, false, kTgUpdate, __half>(x, tiles, st);
+    rc = last ? launch<kTgBatched, true, false, kTgUpdateOut, __half>(x, tiles, st)
+              : launch<kTgBatched, true, false, kTgUpdate, __half>(x, tiles, st);
     if (rc) return rc;
   }
   return MOE_OK;

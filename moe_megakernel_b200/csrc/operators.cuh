@@ -139,11 +139,12 @@ struct OrthoParams {
   const void* g;
   long long ldg, bsg;
   int m, n;
+  int tall;          // m > n: X is G^T, its rows the short side
   float xs, eps;
   double* partial;   // [batch, kOrthoChunks]
   float* alpha;      // [batch]
   __half* hi;
-  uint8_t* lo;       // fp32 gradients only, in pieces (tg_low_at's order)
+  uint8_t* lo;       // fp32 gradients, in pieces (tg_low_at's order), or null
   long long ldx, bsx, lo_bs;
   int chunks;
 };
@@ -274,8 +275,20 @@ __global__ void __launch_bounds__(256) moe_ortho_scale_bf16_kernel(const OrthoPa
   }
 }
 
-// fp32: a warp turns 32 x 32 pieces into the update epilogue's order.
-__global__ void __launch_bounds__(256) moe_ortho_scale_fp32_kernel(const OrthoParams p) {
+// Two neighbouring entries of a row, the second zero past its end.
+__device__ __forceinline__ float2 ortho_pair(const float* p, bool second) { return make_float2(p[0], second ? p[1] : 0.f); }
+__device__ __forceinline__ float2 ortho_pair(const bf16* p, bool second) {
+  if (second && (reinterpret_cast<uintptr_t>(p) & 3) == 0)
+    return TgPair<bf16>::unpack(*reinterpret_cast<const uint32_t*>(p));
+  return make_float2((float)p[0], second ? (float)p[1] : 0.f);
+}
+
+// fp32 gradients, and tall ones, which are transposed on the way: a warp turns
+// 32 x 32 pieces of X into the update epilogue's order. 64 tall matrices of 2048 x
+// 768 in bf16: 88 us for 403 MB (one entry at a time instead of 16-byte vectors
+// and ldmatrix 209 us; without the transposition 80 us).
+template <typename T>
+__global__ void __launch_bounds__(256) moe_ortho_scale_pieces_kernel(const OrthoParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tg_after_stream();
   __shared__ double scratch[8];
@@ -283,39 +296,74 @@ __global__ void __launch_bounds__(256) moe_ortho_scale_fp32_kernel(const OrthoPa
   const double scale = ortho_scale(p, scratch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t piece = ptx::smem_u32(stage[warp]);
-  const float* g = reinterpret_cast<const float*>(p.g) + blockIdx.y * p.bsg;
+  const T* g = reinterpret_cast<const T*>(p.g) + blockIdx.y * p.bsg;
   __half* hi = p.hi + blockIdx.y * p.bsx;
-  uint8_t* lo = p.lo + blockIdx.y * p.lo_bs;
-  const int across = (p.n + 31) / 32, pieces = across * ((p.m + 31) / 32);
+  const int rows = p.tall ? p.n : p.m, cols = p.tall ? p.m : p.n;   // of X
+  const bool vectors = sizeof(T) == 2 && p.tall && ortho_wide<T>(p);
+  const int across = (cols + 31) / 32, pieces = across * ((rows + 31) / 32);
   for (int at = blockIdx.x * 8 + warp; at < pieces; at += gridDim.x * 8) {
     const int r0 = at / across * 32, c0 = (at - at / across * across) * 32;
-    float f[32];
+    float2 f[16];
+    if (vectors) {   // rows of G as 16-byte vectors, turned by ldmatrix
+      const int c = lane & 3;
+      uint4 raw[4];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {   // value j: 8 x 8 block j / 2 (n block j / 8, m block j / 2 % 4), row parity j % 2
-      const int row = r0 + 8 * (j >> 3) + 2 * (lane & 3) + (j & 1), col = c0 + 8 * ((j >> 1) & 3) + (lane >> 2);
-      f[j] = row < p.m && col < p.n ? g[(long long)row * p.ldg + col] : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const int col = c0 + 8 * i + (lane >> 2), row = r0 + 8 * c;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (col < cols && row < rows) raw[i] = *reinterpret_cast<const uint4*>(g + (long long)col * p.ldg + row);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(stage[warp] + tg_piece_at(8 * i + (lane >> 2), c)) = raw[i];
+      __syncwarp();
+      uint32_t v[16];
+      tg_piece_get<kRowsM>(piece, v, lane);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = TgPair<bf16>::unpack(v[j]);
+    }
+    // 8 x 8 block j (row block j / 4, column block j % 4): two rows, one column of X
+    const int row0 = r0 + 2 * (lane & 3), col0 = c0 + (lane >> 2);
+    if (!vectors && p.tall) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int row = row0 + 8 * (j >> 2), col = col0 + 8 * (j & 3);
+        f[j] = make_float2(0.f, 0.f);
+        if (col < cols && row < rows) f[j] = ortho_pair(g + (long long)col * p.ldg + row, row + 1 < rows);
+      }
+    } else if (!vectors) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int row = row0 + 8 * (j >> 2), col = col0 + 8 * (j & 3);
+        f[j] = make_float2(0.f, 0.f);
+        if (col < cols && row < rows) f[j].x = ortho_value(g + (long long)row * p.ldg + col);
+        if (col < cols && row + 1 < rows) f[j].y = ortho_value(g + (long long)(row + 1) * p.ldg + col);
+      }
     }
     uint32_t v[16], w[8];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
+    for (int j = 0; j < 16; j += 2) {
       int q[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float x = (float)(f[j + 2 * h] * scale), y = (float)(f[j + 2 * h + 1] * scale);
-        v[(j >> 1) + h] = TgPair<__half>::pack(x, y);
-        const float2 n = TgPair<__half>::unpack(v[(j >> 1) + h]);
+        const float x = (float)(f[j + h].x * scale), y = (float)(f[j + h].y * scale);
+        v[j + h] = TgPair<__half>::pack(x, y);
+        const float2 n = TgPair<__half>::unpack(v[j + h]);
         q[2 * h] = tg_low(x, n.x);
         q[2 * h + 1] = tg_low(y, n.y);
       }
-      w[j >> 2] = tg_low4(q[0], q[1], q[2], q[3]);
+      w[j >> 1] = tg_low4(q[0], q[1], q[2], q[3]);
     }
-    uint4* out = reinterpret_cast<uint4*>(lo + ((long long)(r0 >> 5) * (p.ldx >> 5) + (c0 >> 5)) * 1024 + lane * 32);
-    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (p.lo != nullptr) {
+      uint4* out = reinterpret_cast<uint4*>(p.lo + blockIdx.y * p.lo_bs +
+                                            ((long long)(r0 >> 5) * (p.ldx >> 5) + (c0 >> 5)) * 1024 + lane * 32);
+      out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
     __syncwarp();
     tg_piece_put<kRowsN>(piece, v, lane);
     __syncwarp();
-    tg_piece_out(piece, hi + (long long)r0 * p.ldx + c0, p.ldx, p.m - r0, 32, lane);
+    tg_piece_out(piece, hi + (long long)r0 * p.ldx + c0, p.ldx, rows - r0, 32, lane);
   }
 }
 

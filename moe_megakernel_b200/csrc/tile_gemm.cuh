@@ -28,7 +28,7 @@
 // shared by few pairs at a time a k block takes 600 to 750 cycles. 8192 x 4096 ->
 // 14336 features, bf16: 609 us (1.58 PFLOP/s) in a burst and 718 us (1.34) under
 // the 1 kW cap, where the clock settles near 1.2 GHz; the library's plain product
-// of the same matrices 628 and 716 us on the same box. Tensor pipe busy 85 to 89 %
+// of the same matrices 628 and 716 us on the same GPU. Tensor pipe busy 85 to 89 %
 // of the cycles (dense 4096 x 4096 -> 14336 and 128 uneven groups, ncu). Tiles of
 // 256 columns are the largest with two accumulators in TMEM; smaller ones load
 // more a FLOP (see pick_tile in operators.cu).
@@ -64,8 +64,8 @@ enum TgEpilogue : int {
   kTgStore = 0,     // act(acc + bias) + residual, the pre-activation kept on request
   kTgGram = 1,      // Newton-Schulz: A = X X^T, scaled
   kTgPoly = 2,      // B = b A + c A A
-  kTgUpdate = 3,    // X' = a X + B X (X as a pair of fp16 values)
-  kTgUpdateOut = 4, // the same, stored as bf16 at the caller's place
+  kTgUpdate = 3,    // X' = a X + B X (X as fp16 and 8 bits more)
+  kTgUpdateOut = 4, // the same, stored as bf16 at the caller's place, transposed on request
   kTgPlain = 5,     // the accumulator alone (gradients)
 };
 
@@ -85,7 +85,7 @@ struct TgParams {
   CUtensorMap tm_out;    // {m, n, batch} box {32, 32}: one piece of the epilogue (not kTgUpdateOut)
   int M, N, K;           // extents (N: rows of Q in a ragged-N product; K: rows in a ragged-K one)
   int groups;            // groups or batches
-  int nt;                // largest N tile: 32, 64, 128 or 256
+  int nt;                // largest N tile, a multiple of 32 up to 256
   int stages, stage_bytes, epi_bytes;
   int f16;               // operands are fp16 (else bf16)
   const int32_t* offsets;   // [groups + 1] device, or null
@@ -106,6 +106,7 @@ struct TgParams {
   long long ldi, in_bs, lo_bs;
   TgFactors factors;
   int backwards;            // batches from the last to the first
+  int transposed;           // kTgUpdateOut: rows m of n
 };
 
 struct TgTask {
@@ -572,10 +573,10 @@ __device__ __forceinline__ void tg_act_all(uint32_t (&r)[2][16], int act) {
 // by 32 N columns. tcgen05.ld.16x256b hands each thread, for every 8 x 8 block,
 // two neighbouring n of one m - the fragment that stmatrix and ldmatrix move to
 // and from shared memory, transposed on request. So the piece is turned to
-// output order (n rows of contiguous m) by four stmatrix, copied out as 16-byte
-// vectors (8 rows of 64 bytes per instruction), and what the epilogue reads (the
-// residual, X, A) comes in the same way, copied ahead with cp.async. Storing
-// straight from a 32x32b load took about 490 instructions a piece, mostly lane
+// output order (n rows of contiguous m) by four stmatrix and stored by one TMA
+// copy (16-byte vectors where a group ends inside it), and what the epilogue
+// reads (the residual, X, A) comes in the same way, copied ahead with cp.async.
+// Storing straight from a 32x32b load took about 490 instructions a piece, mostly lane
 // swaps and addresses, and held the weight gradient at 1.6 TB/s.
 //
 // A piece in shared memory: 32 rows of 64 bytes, the row's 16-byte chunk c at
@@ -888,16 +889,23 @@ __device__ __forceinline__ void tg_piece_store(uint32_t slot, const uint32_t (&v
     return;
   }
   if (mcol <= 0 || nrow <= 0) return;
-  tg_piece_put<kRowsN>(slot, v, lane);
   if (Epi == kTgUpdateOut) {
+    if (p.transposed) tg_piece_put<kRowsM>(slot, v, lane);
+    else tg_piece_put<kRowsN>(slot, v, lane);
     __syncwarp();
-    bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs + (long long)row0 * p.ldo + m;
-    if (p.ldo % 8 == 0 && p.M % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0)
-      tg_piece_out(slot, o, p.ldo, nrow, mcol, lane);
+    const int rows = p.transposed ? mcol : nrow, cols = p.transposed ? nrow : mcol;
+    bf16* o = reinterpret_cast<bf16*>(p.out) + k.g * p.out_bs +
+              (p.transposed ? (long long)m * p.ldo + row0 : (long long)row0 * p.ldo + m);
+    // the row's length is a multiple of 8 where the rest of it from here is
+    if (p.ldo % 8 == 0 && cols % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0)
+      tg_piece_out(slot, o, p.ldo, rows, cols, lane);
     else
-      tg_piece_out_any(slot, reinterpret_cast<uint16_t*>(o), p.ldo, min(nrow, 32), mcol, lane);
+      tg_piece_out_any(slot, reinterpret_cast<uint16_t*>(o), p.ldo, min(rows, 32), cols, lane);
     __syncwarp();
-  } else if (Mode == kTgRaggedN && nrow < 32 && row0 + nrow != p.N) {   // the group ends inside the piece
+    return;
+  }
+  tg_piece_put<kRowsN>(slot, v, lane);
+  if (Mode == kTgRaggedN && nrow < 32 && row0 + nrow != p.N) {   // the group ends inside the piece
     __syncwarp();
     tg_piece_out(slot, reinterpret_cast<T*>(p.out) + (long long)row0 * p.ldo + m, p.ldo, nrow, mcol, lane);
     __syncwarp();

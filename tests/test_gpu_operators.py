@@ -345,7 +345,7 @@ def gradient(*shape, seed, dtype=torch.float32, rank=4):
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (5, 3), (33, 64), (64, 33), (129, 250), (250, 129),
                                    (256, 256), (3, 130, 70), (5, 40, 300), (2, 513, 257), (300, 1031), (1000, 520),
-                                   (40, 300, 520), (40, 520, 300), (90, 130, 140), (300, 20, 33), (58, 28, 1835)])
+                                   (40, 300, 520), (40, 520, 300), (90, 130, 140), (7, 2375, 30), (300, 20, 33), (58, 28, 1835)])
 def test_orthogonalize(shape, dtype):
     G = gradient(*shape, seed=61, dtype=dtype, rank=min(4, *shape[-2:]))
     ortho_close(mk.orthogonalize(G), G)
@@ -388,6 +388,14 @@ def test_orthogonalize_steps_coefficients_and_pitches():
     ortho_close(got, G, coeffs=sched)
     assert (store[:, 0] == 7).all() and (store[:, 58:] == 7).all()
     assert (store[:, :, :3] == 7).all() and (store[:, :, 96:] == 7).all()
+    tall = gradient(3, 130, 80, seed=76)[:2, 5:112, 7:72]
+    for dtype in (torch.float32, BF):
+        src = tall.to(dtype) if dtype == BF else tall
+        wide = torch.full((2, 110, 72), 7.0, dtype=BF, device="cuda")
+        mk.orthogonalize(src, out=wide[:, 2:109, 4:69])
+        ortho_close(wide[:, 2:109, 4:69], src)
+        assert (wide[:, :2] == 7).all() and (wide[:, 109:] == 7).all()
+        assert (wide[:, :, :4] == 7).all() and (wide[:, :, 69:] == 7).all()
     one = gradient(40, 90, seed=75)
     ortho_close(mk.orthogonalize(one, steps=1, coeffs=(1.5, -0.5, 0.0)), one, steps=1, coeffs=(1.5, -0.5, 0.0))
 

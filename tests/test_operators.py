@@ -100,6 +100,7 @@ def test_orthogonalize_workspace(lib):
     assert f(0, 4, 4) == 0 and f(1, 0, 4) == 0
     one, two = f(1, 129, 250), f(2, 129, 250)
     assert one >= 2 * 129 * 256 * 2 + 129 * 256 + 2 * 129 * 192 * 2 and one % 256 == 0
+    assert f(1, 250, 129) == one
     assert one < two <= 2 * one
 
 
