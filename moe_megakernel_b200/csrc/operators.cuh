@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(256) moe_ortho_scale_pieces_kernel(const Ortho
         raw[i] = make_uint4(0, 0, 0, 0);
         if (col < cols && row < rows) raw[i] = *reinterpret_cast<const uint4*>(g + (long long)col * p.ldg + row);
       }
+      __syncwarp();   // every lane has read the piece before
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4*>(stage[warp] + tg_piece_at(8 * i + (lane >> 2), c)) = raw[i];
