@@ -38,9 +38,11 @@ __device__ __forceinline__ float act_slope(float z) {
     return fmaf(z, density, phi);
   }
   if (Act == kActGeluTanh) {
-    const float w = 0.044715f * z * z;
+    // q(v) + z q (1 - q) v'(z). z q (1 - q) is formed first and v' bounded (from |z| = 473 on, long after
+    // q is 0 or 1): a zero then never meets an infinity, however large z is
+    const float w = fminf(0.044715f * z * z, 1e4f);
     const float q = tg_sigmoid(1.59576912160573071f * fmaf(w, z, z));
-    return q * fmaf(z * (1.f - q) * 1.59576912160573071f, fmaf(3.f, w, 1.f), 1.f);
+    return fmaf(q * (1.f - q) * z, 1.59576912160573071f * fmaf(3.f, w, 1.f), q);
   }
   if (Act == kActSilu) {
     const float q = tg_sigmoid(z);

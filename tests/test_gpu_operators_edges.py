@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import moe_megakernel_b200 as mk
-from tests.test_gpu_operators import BF, gradient, ortho_close
+from tests.test_gpu_operators import BF, HF, U, act64, gradient, ortho_close, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -18,3 +18,46 @@ def test_orthogonalize_batches_with_several_pieces_to_a_warp(shape, dtype):
     out = mk.orthogonalize(G)
     for at in range(0, shape[0], 400):
         ortho_close(out[at:at + 400], G[at:at + 400])
+
+
+FAR = [0.0, 1e-30, 0.25, 0.75, 2.0, 7.5, 20.0, 100.0, 3000.0, 6e4, 1e9, 1.5e13, 4e13, 1e16, 8e19, 1e25, 1e30, 3.3e38]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_slopes_of_far_preactivations(act, dtype):
+    """Up to the type's largest value a slope is a number: 0 or 1 where the activation has gone flat or
+    straight, and no NaN gets from one pre-activation into a row of dx or a column of dW. Tolerance: the
+    rounding, and 1e-5 for the fp32 evaluation (an exponential good to 2 + 1.17 |v| units of 2^-23, whose
+    weight in a slope, |z v'| e^-|v|, is below 1.2)."""
+    z = torch.tensor([s * v for v in FAR if dtype == BF or v < 65504 for s in (1, -1)], device="cuda", dtype=dtype)
+    z = torch.cat([z, z.new_zeros(-len(z) % 8)])
+    N = len(z)
+    x, W = torch.zeros(1, 8, dtype=dtype, device="cuda"), torch.ones(8, N, dtype=dtype, device="cuda")
+    x[0, 3] = 1
+    dy = torch.ones(1, N, dtype=dtype, device="cuda")
+    g = mk.linear_backward(dy, x, W, preact=z[None], activation=act, bias_grad=True)
+    ref = slope64(z.double(), act)
+    for name, got in (("dbias", g["dbias"]), ("dW", g["dW"][3])):
+        off = (got.double() - ref).abs()
+        assert (off <= U[dtype] * ref.abs() + 1e-5).all(), (name, z[~(off <= U[dtype] * ref.abs() + 1e-5)])
+    assert (g["dW"][:3] == 0).all() and (g["dW"][4:] == 0).all()
+    assert ((g["dx"].double() - ref.sum()).abs() <= 2 * U[dtype] * ref.abs().sum() + 1e-5 * N).all()
+
+
+@pytest.mark.parametrize("T", [1, 700])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_activations_of_far_preactivations(act, T):
+    """The same for the values, through both kernels, and NaN stays NaN. Tolerance as above: an
+    activation's own weight |z| e^-|v| is below 1.2 as well."""
+    z = torch.tensor([s * v for v in FAR for s in (1, -1)] + [float("nan")] * 4, device="cuda", dtype=BF)
+    W = torch.zeros(8, len(z), dtype=BF, device="cuda")
+    x = torch.zeros(T, 8, dtype=BF, device="cuda")
+    x[:, 5] = 1
+    b = z.clone()          # z = 0 + b: exact
+    y, kept = mk.linear(x, W, bias=b, activation=act, save_preact=True)
+    ref = act64(z.double(), act)
+    number = ~z.isnan()
+    assert torch.equal(kept[:, number], z[number].expand(T, -1)) and kept[:, ~number].isnan().all()
+    assert y[:, ~number].isnan().all()
+    assert ((y.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5)[:, number].all()
