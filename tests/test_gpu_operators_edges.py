@@ -1,4 +1,6 @@
 """The operators around the layer at the edges of what they take, against 64-bit formulas."""
+import math
+
 import pytest
 import torch
 
@@ -61,3 +63,40 @@ def test_activations_of_far_preactivations(act, T):
     assert torch.equal(kept[:, number], z[number].expand(T, -1)) and kept[:, ~number].isnan().all()
     assert y[:, ~number].isnan().all()
     assert ((y.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5)[:, number].all()
+
+
+def tail64(z, act):
+    """An activation, without the cancellation of 1 + tanh(u) at the far negative end: z / (1 + e^(-2u))."""
+    if act != "gelu_tanh":
+        return act64(z, act)
+    return z * torch.sigmoid(math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("T", [1, 600])
+def test_activations_keep_their_small_values(act, T, dtype):
+    """Every z of the type in -12 .. 6 (fp16: every eighth): the value and the slope are off by the rounding
+    and 2^-15 of themselves, however small they are. 2^-15 = 3e-5: the exponential is good to 2 + 1.17 |v|
+    units of 2^-23 (|v| <= 72: 1e-5 at most) and its argument is rounded three times
+    (3 |v| 2^-24: 1.3e-5 at most). A slope's two terms cancel around z = -1, so its error counts against
+    their magnitudes; fp16 values below 2^-14 are rounded in steps of 2^-24."""
+    i = torch.arange(-32768, 32768, dtype=torch.int32, device="cuda").to(torch.int16)
+    z = i.view(dtype)
+    z = z[(z >= (-12 if act != "gelu_tanh" else -9)) & (z <= 6) & (z.abs() >= 2.0 ** -13)]
+    z = z[::8 if dtype == HF else 1]
+    z = z[:len(z) // 8 * 8].contiguous()
+    W, x = torch.zeros(8, len(z), dtype=dtype, device="cuda"), torch.zeros(T, 8, dtype=dtype, device="cuda")
+    ones = torch.ones(T, len(z), dtype=dtype, device="cuda")
+    tiny = 2.0 ** -25 if dtype == HF else 0.0
+    y = mk.linear(x, W, bias=z, activation=act)
+    z64 = z.double().requires_grad_()
+    value = tail64(z64, act)
+    slope, = torch.autograd.grad(value.sum(), z64)
+    value = value.detach()
+    assert ((y.double() - value).abs() <= (U[dtype] + 2.0 ** -15) * value.abs() + tiny).all()
+    x[0, 0] = 1            # dW[0] is the first row's dz
+    got = mk.linear_backward(ones, x, W, preact=z.expand(T, -1).contiguous(), activation=act)["dW"][0].double()
+    parts = (value / z.double()).abs()    # q, or Phi
+    parts = parts + (slope - parts).abs()
+    assert ((got - slope).abs() <= U[dtype] * slope.abs() * 1.01 + 2.0 ** -15 * parts + 2 * tiny).all()
