@@ -100,3 +100,19 @@ def test_activations_keep_their_small_values(act, T, dtype):
     parts = (value / z.double()).abs()    # q, or Phi
     parts = parts + (slope - parts).abs()
     assert ((got - slope).abs() <= U[dtype] * slope.abs() * 1.01 + 2.0 ** -15 * parts + 2 * tiny).all()
+
+
+@pytest.mark.parametrize("T", [1, 600])
+def test_silu_keeps_its_smallest_values(T):
+    """silu and its slope down to z = -90, where they are near bf16's smallest normal number: the rounding
+    (below that number half a step, 2^-134), and 2^-15 for an exponential good to 2 + 1.17 * 90 units of 2^-23."""
+    z = torch.linspace(-90, -12, 1000, device="cuda").to(BF)
+    W, x = torch.zeros(8, len(z), dtype=BF, device="cuda"), torch.zeros(T, 8, dtype=BF, device="cuda")
+    y = mk.linear(x, W, bias=z, activation="silu")
+    ref = act64(z.double(), "silu")
+    assert ((y.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -15) * ref.abs() + 2.0 ** -134).all()
+    x[0, 0] = 1
+    got = mk.linear_backward(torch.ones(T, len(z), dtype=BF, device="cuda"), x, W, preact=z.expand(T, -1).contiguous(),
+                             activation="silu")["dW"][0].double()
+    ref = slope64(z.double(), "silu")
+    assert ((got - ref).abs() <= (2.0 ** -8 + 2.0 ** -14) * ref.abs() + 2.0 ** -133).all()
