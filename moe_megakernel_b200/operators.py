@@ -5,8 +5,13 @@ Argument checks and marshalling over the C entry points of the same names
 (include/moe_b200.h); every step runs in the library's CUDA kernels. Tensors
 are bf16 or fp16 on one CUDA device, the last index contiguous, rows a multiple
 of 8 elements apart. Work is enqueued on `stream` (default: the current stream
-of the tensors' device); nothing synchronises. `error_word`, an int32 tensor of
-one element, receives the call's device error code (0 = none).
+of the tensors' device); nothing synchronises. With a `stream` of its own a call
+takes the tensors that it makes (results and scratch) from the allocator on that
+stream; its inputs have to be ready there, and a result that another stream goes
+on with needs what any tensor needs there: that stream waits, and
+``Tensor.record_stream`` if the result may be dropped before that work is done.
+`error_word`, an int32 tensor of one element, receives the call's device error
+code (0 = none).
 """
 from __future__ import annotations
 
@@ -94,7 +99,11 @@ def _error_word(t, device):
 
 
 def _raw_stream(stream, device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream: expected a stream of {device}, got one of {stream.device}")
+    return stream.cuda_stream
 
 
 def _call(name: str, device, *args):
@@ -109,15 +118,18 @@ def _call(name: str, device, *args):
         raise MoEError(rc, name)
 
 
-def _workspace(nbytes: int, device, stream):
-    """Scratch of one call, taken from the allocator on the stream that uses it (so that it is
-    reused only by later work of that stream, and belongs to the graph when captured)."""
-    if not nbytes:
-        return None
+def _new(like, shape, stream, dtype=None):
+    """A tensor beside ``like`` from the allocator, for work on ``stream``: taken on that stream, so that
+    the memory held nothing which work still queued on another one reads, and so that it is reused only
+    behind that stream's work (and belongs to the graph when captured)."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(nbytes: int, like, stream):
+    return _new(like, (nbytes,), stream, torch.uint8) if nbytes else None
 
 
 def _offsets(offsets, device):
@@ -149,7 +161,7 @@ def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, tran
     _whole(W, "W", (groups, N, K) if transpose else (groups, K, N), x.dtype, dev)
     _cuda(x, "x")
     if y is None:
-        y = x.new_empty((rows, N))
+        y = _new(x, (rows, N), stream)
     else:
         _like(y, "y", (rows, N), x.dtype, dev)
     _call("moe_grouped_matmul", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), offsets.data_ptr(), rows, groups, K, N,
@@ -174,7 +186,7 @@ def grouped_matmul_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tenso
     _like(dy, "dy", (rows, N), x.dtype, dev)
     _cuda(x, "x")
     if dW is None:
-        dW = x.new_empty((groups, K, N))
+        dW = _new(x, (groups, K, N), stream)
     else:
         _whole(dW, "dW", (groups, K, N), x.dtype, dev)
     _call("moe_grouped_matmul_wgrad", dev, x.data_ptr(), _pitch(x, "x"), dy.data_ptr(), _pitch(dy, "dy"),
@@ -205,13 +217,13 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
         _like(residual, "residual", (T, N), x.dtype, dev)
     _cuda(x, "x")
     if y is None:
-        y = x.new_empty((T, N))
+        y = _new(x, (T, N), stream)
     else:
         _like(y, "y", (T, N), x.dtype, dev)
     if preact is not None:
         _like(preact, "preact", (T, N), x.dtype, dev)
     elif save_preact:
-        preact = x.new_empty((T, N))
+        preact = _new(x, (T, N), stream)
     _call("moe_linear", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), _address(bias), _address(residual),
           0 if residual is None else _pitch(residual, "residual"), T, K, N, act, dt, y.data_ptr(), _pitch(y, "y"),
           _address(preact), 0 if preact is None else _pitch(preact, "preact"), _error_word(error_word, dev),
@@ -242,11 +254,11 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, preact: 
         _like(z, "preact", (T, N), x.dtype, dev)
     _cuda(x, "x")
     lib = load_library()
-    dx = x.new_empty((T, K)) if input_grad else None
-    dW = x.new_empty((K, N)) if weight_grad else None
-    dbias = x.new_empty((N,)) if bias_grad else None
+    dx = _new(x, (T, K), stream) if input_grad else None
+    dW = _new(x, (K, N), stream) if weight_grad else None
+    dbias = _new(x, (N,), stream) if bias_grad else None
     nbytes = lib.moe_linear_backward_workspace_bytes(T, N, act, 1 if bias_grad else 0)
-    ws = _workspace(nbytes, dev, stream)
+    ws = _workspace(nbytes, x, stream)
     _call("moe_linear_backward", dev, dy.data_ptr(), _pitch(dy, "dy"), x.data_ptr(), _pitch(x, "x"), W.data_ptr(),
           _address(z), 0 if z is None else _pitch(z, "preact"), T, K, N, act, dt, _address(dx), K, _address(dW),
           _address(dbias), _address(ws), nbytes, _error_word(error_word, dev), _raw_stream(stream, dev))
@@ -284,7 +296,7 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
     _cuda(G, "G")
     dev = G.device
     if out is None:
-        out = torch.empty(G.shape, dtype=torch.bfloat16, device=dev)
+        out = _new(G, G.shape, stream, torch.bfloat16)
     else:
         _like(out, "out", tuple(G.shape), torch.bfloat16, dev)
 
@@ -299,7 +311,7 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
     batch, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
     lib = load_library()
     nbytes = lib.moe_orthogonalize_workspace_bytes(batch, m, n)
-    ws = _workspace(nbytes, dev, stream)
+    ws = _workspace(nbytes, G, stream)
     _call("moe_orthogonalize", dev, G.data_ptr(), *pitches(G, "G"), batch, m, n, DTYPE_CODES[G.dtype], steps, flat, eps,
           out.data_ptr(), *pitches(out, "out"), _address(ws), nbytes, _error_word(error_word, dev),
           _raw_stream(stream, dev))

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import moe_megakernel_b200 as mk
-from tests.test_gpu_operators import BF, HF, U, act64, gradient, ortho_close, slope64
+from tests.test_gpu_operators import BF, HF, U, act64, gradient, offsets_of, ortho_close, rand, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,39 @@ def test_silu_keeps_its_smallest_values(T):
                              activation="silu")["dW"][0].double()
     ref = slope64(z.double(), "silu")
     assert ((got - ref).abs() <= (2.0 ** -8 + 2.0 ** -14) * ref.abs() + 2.0 ** -133).all()
+
+
+def _stream_calls():
+    x, W = rand(300, 512, seed=141), rand(512, 264, seed=142, std=0.05)
+    Wg, off, dy = rand(4, 512, 264, seed=143, std=0.05), offsets_of([100, 0, 150, 50]), rand(300, 264, seed=144)
+    G = gradient(512, 264, seed=145)
+    return {
+        "grouped_matmul": ((300, 264), lambda s: mk.grouped_matmul(x, Wg, off, stream=s)),
+        "grouped_matmul_wgrad": ((4, 512, 264), lambda s: mk.grouped_matmul_wgrad(x, dy, off, stream=s)),
+        "linear": ((300, 264), lambda s: mk.linear(x, W, stream=s)),
+        "linear_backward": ((512, 264), lambda s: mk.linear_backward(dy, x, W, input_grad=False, stream=s)["dW"]),
+        "orthogonalize": ((512, 264), lambda s: mk.orthogonalize(G, stream=s)),
+    }
+
+
+@pytest.mark.parametrize("name", ["grouped_matmul", "grouped_matmul_wgrad", "linear", "linear_backward", "orthogonalize"])
+def test_results_on_an_explicit_stream_take_no_other_streams_memory(name):
+    """A result written on a side stream neither lands in a block that the current stream's queued work
+    still reads, nor, dropped at once, is its block handed to the current stream while the kernel runs."""
+    shape, call = _stream_calls()[name]
+    side = torch.cuda.Stream()
+    ref = call(None)
+    torch.cuda.synchronize()
+    a, b = (torch.full(shape, v, dtype=BF, device="cuda") for v in (7.0, 0.0))
+    torch.cuda._sleep(40_000_000)      # some 20 ms
+    b.copy_(a)
+    del a
+    y = call(side)
+    torch.cuda.synchronize()
+    assert (b == 7).all() and torch.equal(y, ref)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    call(side)                         # dropped
+    c = torch.full(shape, 7.0, dtype=BF, device="cuda")
+    torch.cuda.synchronize()
+    assert (c == 7).all()

@@ -1,0 +1,76 @@
+"""The operators around the layer, what can be seen of them without a GPU."""
+import contextlib
+
+import pytest
+import torch
+
+import moe_megakernel_b200 as mk
+from moe_megakernel_b200 import operators
+from tests.test_operators import BF, _off, _z
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from moe_megakernel_b200 import build, load_library
+    build.build()
+    return load_library()
+
+
+class Stream:
+    """Stands for a stream of the tensors' device (here the host)."""
+    cuda_stream = 5
+    device = torch.device("cpu")
+
+
+CALLS = {
+    "grouped_matmul": lambda s: mk.grouped_matmul(_z(4, 64), _z(2, 64, 32), _off(0, 2, 4), stream=s),
+    "grouped_matmul_wgrad": lambda s: mk.grouped_matmul_wgrad(_z(4, 64), _z(4, 32), _off(0, 2, 4), stream=s),
+    "linear": lambda s: mk.linear(_z(4, 64), _z(64, 32), save_preact=True, stream=s),
+    "linear_backward": lambda s: mk.linear_backward(_z(4, 32), _z(4, 64), _z(64, 32), preact=_z(4, 32), activation="silu",
+                                                    bias_grad=True, stream=s),
+    "orthogonalize": lambda s: mk.orthogonalize(_z(4, 6), stream=s),
+}
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The C calls are noted down instead of made; argument checks that need a GPU pass."""
+    made = []
+    monkeypatch.setattr(operators, "_cuda", lambda t, name: None)
+    monkeypatch.setattr(operators, "_call", lambda name, device, *args: made.append((name, args)))
+    return made
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_results_are_allocated_on_the_stream_that_writes_them(name, calls, monkeypatch):
+    """A block of another stream's pool may still be read by work queued there."""
+    inside, made = [], []
+    stream = Stream()
+
+    @contextlib.contextmanager
+    def on(s):
+        inside.append(s)
+        yield
+        inside.pop()
+
+    def noted(f):
+        def g(*args, **kw):
+            made.append(list(inside))
+            return f(*args, **kw)
+        return g
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.Tensor, "new_empty", noted(torch.Tensor.new_empty))
+    monkeypatch.setattr(torch, "empty", noted(torch.empty))
+    CALLS[name](stream)
+    assert made and all(m == [stream] for m in made)
+    assert calls[0][0] == "moe_" + name and calls[0][1][-1] == 5
+
+
+def test_streams_of_other_devices_are_refused(calls):
+    class Other(Stream):
+        device = torch.device("cuda", 1)
+    for call in CALLS.values():
+        with pytest.raises(ValueError, match="stream"):
+            call(Other())
+    assert not calls
