@@ -7,6 +7,7 @@ the binding fails loudly; there is no other implementation to fall back to.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -144,6 +145,12 @@ def _stream_handle(stream, device) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on(stream):
+    """Allocations for work on ``stream`` are taken on it: the memory then held nothing that work still
+    queued on another stream reads, and is reused only behind that stream's work."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _check(t: torch.Tensor, name: str, shape, dtype, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -215,7 +222,8 @@ class MoEPlan:
         """Ws1/Ws3/Ws2: the shared experts' weights, required when the plan has n_shared > 0."""
         T = self._check_inputs(x, Wg, bias, (W1, W3, W2), (Ws1, Ws3, Ws2))
         if y is None:
-            y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            with _on(stream):
+                y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         _check(y, "y", (T, self.H), torch.bfloat16, self.device)
         _ok(self.lib.moe_forward_shared(self._plan, _ptr(x), _ptr(Wg), _ptr(bias), _ptr(W1), _ptr(W3), _ptr(W2),
                                         _ptr(Ws1), _ptr(Ws3), _ptr(Ws2), T, _ptr(y),
@@ -248,7 +256,8 @@ class MoEPlan:
         T = self._check_inputs(x, Wg, bias)
         self._check_fp8(W1q, s1, W3q, s3, W2q, s2)
         if y is None:
-            y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            with _on(stream):
+                y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         _check(y, "y", (T, self.H), torch.bfloat16, self.device)
         _ok(self.lib.moe_forward_fp8(self._plan, _ptr(x), _ptr(Wg), _ptr(bias), _ptr(W1q), _ptr(s1), _ptr(W3q),
                                      _ptr(s3), _ptr(W2q), _ptr(s2), T, _ptr(y), _stream_handle(stream, self.device)),
@@ -307,12 +316,13 @@ class MoEPlan:
         o = dict(out) if out is not None else {}
         dev = self.device
         E, H, I = self.E, self.H, self.I
-        o.setdefault("dx", torch.empty((T, H), dtype=torch.bfloat16, device=dev))
-        o.setdefault("dWg", torch.empty((H, E), dtype=torch.float32, device=dev))
-        o.setdefault("dbias", None if bias is None else torch.empty((E,), dtype=torch.float32, device=dev))
-        o.setdefault("dW1", torch.empty((E, H, I), dtype=torch.bfloat16, device=dev))
-        o.setdefault("dW3", torch.empty((E, H, I), dtype=torch.bfloat16, device=dev))
-        o.setdefault("dW2", torch.empty((E, I, H), dtype=torch.bfloat16, device=dev))
+        with _on(stream):
+            o.setdefault("dx", torch.empty((T, H), dtype=torch.bfloat16, device=dev))
+            o.setdefault("dWg", torch.empty((H, E), dtype=torch.float32, device=dev))
+            o.setdefault("dbias", None if bias is None else torch.empty((E,), dtype=torch.float32, device=dev))
+            o.setdefault("dW1", torch.empty((E, H, I), dtype=torch.bfloat16, device=dev))
+            o.setdefault("dW3", torch.empty((E, H, I), dtype=torch.bfloat16, device=dev))
+            o.setdefault("dW2", torch.empty((E, I, H), dtype=torch.bfloat16, device=dev))
         _check(o["dx"], "dx", (T, H), torch.bfloat16, dev)
         _check(o["dWg"], "dWg", (H, E), torch.float32, dev)
         if o["dbias"] is not None:
@@ -458,8 +468,9 @@ def quantize_weights_fp8(W: torch.Tensor, stream=None):
         raise TypeError("W must be a 3-D torch.Tensor [E, K, N]")
     E, H, I = W.shape
     _check(W, "W", (E, H, I), torch.bfloat16, None)
-    Wq = torch.empty((E, I, H), dtype=torch.uint8, device=W.device)
-    sc = torch.empty((E, I), dtype=torch.float32, device=W.device)
+    with _on(stream):
+        Wq = torch.empty((E, I, H), dtype=torch.uint8, device=W.device)
+        sc = torch.empty((E, I), dtype=torch.float32, device=W.device)
     _ok(load_library().moe_quantize_weights_fp8(_ptr(W), _ptr(Wq), _ptr(sc), E, H, I,
                                                 _stream_handle(stream, W.device)), "moe_quantize_weights_fp8")
     return Wq, sc
@@ -471,8 +482,9 @@ def quantize_x_fp8(x: torch.Tensor, stream=None):
         raise TypeError("x must be a 2-D torch.Tensor [T, H]")
     T, H = x.shape
     _check(x, "x", (T, H), torch.bfloat16, None)
-    xq = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-    sx = torch.empty((T,), dtype=torch.float32, device=x.device)
+    with _on(stream):
+        xq = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+        sx = torch.empty((T,), dtype=torch.float32, device=x.device)
     _ok(load_library().moe_quantize_x_fp8(_ptr(x), _ptr(xq), _ptr(sx), T, H, _stream_handle(stream, x.device)),
         "moe_quantize_x_fp8")
     return xq, sx

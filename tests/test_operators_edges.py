@@ -41,11 +41,10 @@ def calls(monkeypatch):
     return made
 
 
-@pytest.mark.parametrize("name", CALLS)
-def test_results_are_allocated_on_the_stream_that_writes_them(name, calls, monkeypatch):
-    """A block of another stream's pool may still be read by work queued there."""
+@pytest.fixture
+def allocations(monkeypatch):
+    """For every tensor made from here on, the streams that were current."""
     inside, made = [], []
-    stream = Stream()
 
     @contextlib.contextmanager
     def on(s):
@@ -62,8 +61,15 @@ def test_results_are_allocated_on_the_stream_that_writes_them(name, calls, monke
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.Tensor, "new_empty", noted(torch.Tensor.new_empty))
     monkeypatch.setattr(torch, "empty", noted(torch.empty))
+    return made
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_results_are_allocated_on_the_stream_that_writes_them(name, calls, allocations):
+    """A block of another stream's pool may still be read by work queued there."""
+    stream = Stream()
     CALLS[name](stream)
-    assert made and all(m == [stream] for m in made)
+    assert allocations and all(made == [stream] for made in allocations)
     assert calls[0][0] == "moe_" + name and calls[0][1][-1] == 5
 
 
