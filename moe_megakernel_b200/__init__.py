@@ -17,7 +17,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_b200.so")
 
-MOE_OK = 0
+MOE_OK, MOE_ERR_UNSUPPORTED_SHAPE = 0, 2
 STATUS_NAMES = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
     3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_NO_WORKSPACE", 5: "MOE_ERR_CUDA",
@@ -135,6 +135,12 @@ def _ok(rc: int, what: str):
         raise MoEError(rc, what)
 
 
+def _counts(what: str, *counts):
+    """Counts as the C entry points take them: ctypes would drop the upper bits of a larger one."""
+    if max(counts) > 0x7fffffff:
+        raise MoEError(MOE_ERR_UNSUPPORTED_SHAPE, what)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -177,6 +183,7 @@ class MoEPlan:
         self.lib = load_library()
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else torch.device(device).index or 0)
+        _counts("moe_plan_create_shared", T_max, H, I, E, k, n_shared, block_m)
         self.T_max, self.H, self.I, self.E, self.k, self.n_shared = T_max, H, I, E, k, n_shared
         self._plan = ctypes.c_void_p()
         _ok(self.lib.moe_plan_create_shared(ctypes.byref(self._plan), T_max, H, I, E, k, n_shared, block_m,
@@ -468,6 +475,7 @@ def quantize_weights_fp8(W: torch.Tensor, stream=None):
         raise TypeError("W must be a 3-D torch.Tensor [E, K, N]")
     E, H, I = W.shape
     _check(W, "W", (E, H, I), torch.bfloat16, None)
+    _counts("moe_quantize_weights_fp8", E, H, I)
     with _on(stream):
         Wq = torch.empty((E, I, H), dtype=torch.uint8, device=W.device)
         sc = torch.empty((E, I), dtype=torch.float32, device=W.device)
@@ -482,6 +490,7 @@ def quantize_x_fp8(x: torch.Tensor, stream=None):
         raise TypeError("x must be a 2-D torch.Tensor [T, H]")
     T, H = x.shape
     _check(x, "x", (T, H), torch.bfloat16, None)
+    _counts("moe_quantize_x_fp8", T, H)
     with _on(stream):
         xq = torch.empty((T, H), dtype=torch.uint8, device=x.device)
         sx = torch.empty((T,), dtype=torch.float32, device=x.device)

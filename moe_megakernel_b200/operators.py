@@ -4,7 +4,7 @@ and its gradients, and the orthogonalised update of weight gradients.
 Argument checks and marshalling over the C entry points of the same names
 (include/moe_b200.h); every step runs in the library's CUDA kernels. Tensors
 are bf16 or fp16 on one CUDA device, the last index contiguous, rows a multiple
-of 8 elements apart. Work is enqueued on `stream` (default: the current stream
+of 8 elements apart, no extent above 2**30. Work is enqueued on `stream` (default: the current stream
 of the tensors' device); nothing synchronises. With a `stream` of its own a call
 takes the tensors that it makes (results and scratch) from the allocator on that
 stream; its inputs have to be ready there, and a result that another stream goes
@@ -21,7 +21,7 @@ from typing import Optional, Sequence, Union
 
 import torch
 
-from . import MoEError, load_library
+from . import MOE_ERR_UNSUPPORTED_SHAPE, MoEError, _counts, load_library
 
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -159,6 +159,7 @@ def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, tran
     N = W.shape[1] if transpose else W.shape[2]
     _last(x, "x")
     _whole(W, "W", (groups, N, K) if transpose else (groups, K, N), x.dtype, dev)
+    _counts("moe_grouped_matmul", rows, groups, K, N)
     _cuda(x, "x")
     if y is None:
         y = _new(x, (rows, N), stream)
@@ -184,6 +185,7 @@ def grouped_matmul_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tenso
     groups = _offsets(offsets, dev)
     _last(x, "x")
     _like(dy, "dy", (rows, N), x.dtype, dev)
+    _counts("moe_grouped_matmul_wgrad", rows, groups, K, N)
     _cuda(x, "x")
     if dW is None:
         dW = _new(x, (groups, K, N), stream)
@@ -211,6 +213,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     dev = x.device
     _last(x, "x")
     _whole(W, "W", (K, N), x.dtype, dev)
+    _counts("moe_linear", T, K, N)
     if bias is not None:
         _whole(bias, "bias", (N,), x.dtype, dev)
     if residual is not None:
@@ -247,6 +250,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, preact: 
     _last(x, "x")
     _whole(W, "W", (K, N), x.dtype, dev)
     _like(dy, "dy", (T, N), x.dtype, dev)
+    _counts("moe_linear_backward", T, K, N)
     if act and preact is None:
         raise ValueError("preact is needed with an activation")
     z = preact if act else None
@@ -291,6 +295,10 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
         raise ValueError(f"G: expected bfloat16 or float32, got {G.dtype}")
     if steps < 1:
         raise ValueError("steps must be at least 1")
+    batch, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
+    _counts("moe_orthogonalize", batch, m, n)
+    if steps > 64:
+        raise MoEError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_orthogonalize")
     flat = _schedule(steps, tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coeffs))
     _last(G, "G")
     _cuda(G, "G")
@@ -308,7 +316,6 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
             raise ValueError(f"{name}: rows or matrices overlap")
         return ld, bs
 
-    batch, m, n = G.shape if G.dim() == 3 else (1, *G.shape)
     lib = load_library()
     nbytes = lib.moe_orthogonalize_workspace_bytes(batch, m, n)
     ws = _workspace(nbytes, G, stream)

@@ -80,3 +80,45 @@ def test_streams_of_other_devices_are_refused(calls):
         with pytest.raises(ValueError, match="stream"):
             call(Other())
     assert not calls
+
+
+META = torch.device("meta")
+BIG = 2 ** 32 + 8      # 8 in its lower 32 bits
+
+
+def _m(*shape, dtype=BF):
+    return torch.empty(shape, dtype=dtype, device=META)
+
+
+class MetaStream(Stream):
+    device = META
+
+
+@pytest.mark.parametrize("call", [
+    lambda s: mk.grouped_matmul(_m(BIG, 8), _m(2, 8, 16), _m(3, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul(_m(4, BIG), _m(2, BIG, 16), _m(3, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul(_m(4, 8), _m(2, 8, BIG), _m(3, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul(_m(4, 8), _m(2, BIG, 8), _m(3, dtype=torch.int32), transpose=True, stream=s),
+    lambda s: mk.grouped_matmul(_m(4, 8), _m(BIG, 8, 16), _m(BIG + 1, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul_wgrad(_m(BIG, 8), _m(BIG, 16), _m(3, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul_wgrad(_m(4, BIG), _m(4, 16), _m(3, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul_wgrad(_m(4, 8), _m(4, BIG), _m(3, dtype=torch.int32), stream=s),
+    lambda s: mk.grouped_matmul_wgrad(_m(4, 8), _m(4, 8), _m(BIG + 1, dtype=torch.int32), stream=s),
+    lambda s: mk.linear(_m(BIG, 8), _m(8, 16), stream=s),
+    lambda s: mk.linear(_m(4, BIG), _m(BIG, 16), stream=s),
+    lambda s: mk.linear(_m(4, 8), _m(8, BIG), stream=s),
+    lambda s: mk.linear_backward(_m(BIG, 16), _m(BIG, 8), _m(8, 16), stream=s),
+    lambda s: mk.linear_backward(_m(4, BIG), _m(4, 8), _m(8, BIG), stream=s),
+    lambda s: mk.linear_backward(_m(4, 16), _m(4, BIG), _m(BIG, 16), stream=s),
+    lambda s: mk.orthogonalize(_m(BIG, 4, 4), stream=s),
+    lambda s: mk.orthogonalize(_m(BIG, 4), stream=s),
+    lambda s: mk.orthogonalize(_m(4, BIG), stream=s),
+    lambda s: mk.orthogonalize(_m(4, 4), steps=65, stream=s),
+    lambda s: mk.quantize_x_fp8(_m(BIG, 8), stream=s),
+    lambda s: mk.quantize_weights_fp8(_m(BIG, 64, 64), stream=s),
+    lambda s: mk.MoEPlan(2 ** 32 + 64, 128, 256, 8, 2, device="cuda:0")])
+def test_extents_past_32_bits_are_refused(call, calls):
+    """Not taken for their lower 32 bits, which the C entry would find nothing wrong with."""
+    with pytest.raises(mk.MoEError, match="MOE_ERR_UNSUPPORTED_SHAPE"):
+        call(MetaStream())
+    assert not calls
