@@ -33,6 +33,7 @@ struct FewParams {
   int split, stages;  // parts of the reduction
   int f16;
   int32_t* err;
+  long long wait_cycles;
   void* out;
   long long ldo;
   const void* bias;
@@ -65,7 +66,7 @@ __device__ __forceinline__ bool few_wait(uint64_t* bar, uint32_t parity, const F
     const long long t0 = clock64();
     while (!(ok = tg_try_wait(bar, parity))) {
       if (*reinterpret_cast<volatile int*>(&s.abort)) break;
-      if (clock64() - t0 > kTgTimeoutCycles) {
+      if (clock64() - t0 > p.wait_cycles) {
         if (p.err != nullptr) atomicCAS(p.err, 0, (int)kDevTimeout);
         *reinterpret_cast<volatile int*>(&s.abort) = 1;
         break;

@@ -138,6 +138,7 @@ int launch(TgParams& p, long long tiles, cudaStream_t st) {
     clusters[d].store(c);
   }
   const int bytes = size_stages<Mode, Epi>(p, QMn);
+  p.wait_cycles = tg_wait_cycles(p.K);
   cfg.gridDim = dim3(2 * (unsigned)(tiles > 0 && tiles < c ? tiles : c));
   cfg.dynamicSmemBytes = bytes;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -299,6 +300,7 @@ int launch_few_kind(const TgParams& p, const FewCut& cut, const Operand& P, cons
   f.stages = std::min(kFewMaxStages, most / few_stage_bytes(cols));
   f.f16 = p.f16;
   f.err = p.err;
+  f.wait_cycles = tg_wait_cycles(p.K);
   f.out = p.out;
   f.ldo = p.ldo;
   f.bias = p.bias;

@@ -51,7 +51,11 @@ constexpr int kTgMaxGroups = 1024;
 constexpr int kTgSorted = 256;           // groups that a weight gradient sorts by size
 constexpr int kTgRing = 4;               // tiles worked out ahead
 constexpr int kTgABytes = 128 * 128;     // 128 rows of P, 64 k each
-constexpr long long kTgTimeoutCycles = 4000000000ll;   // about two seconds
+// A wait's bound: about two seconds, and 4096 cycles for each block of 64 of the launch's longest reduction
+// (measured 600 to 1200): the longest wait of a sound call is the epilogue's, for all of a tile's blocks, and a
+// group may have 2^24 of them.
+constexpr long long kTgTimeoutCycles = 4000000000ll, kTgBlockCycles = 4096;
+constexpr long long tg_wait_cycles(long long k) { return kTgTimeoutCycles + (k + 63) / 64 * kTgBlockCycles; }
 
 enum TgMode : int {
   kTgRaggedN = 0,    // groups of N-side rows, one P per group (offsets == null: one group of all rows)
@@ -90,6 +94,7 @@ struct TgParams {
   int f16;               // operands are fp16 (else bf16)
   const int32_t* offsets;   // [groups + 1] device, or null
   int32_t* err;             // device error word, or null
+  long long wait_cycles;    // bound of a wait (tg_wait_cycles of the longest reduction)
   // output
   void* out;
   long long ldo, out_bs;    // row and batch pitch in elements
@@ -172,7 +177,7 @@ __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, const Tg
   const long long t0 = clock64();
   while (!tg_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
-    if (clock64() - t0 > kTgTimeoutCycles) {
+    if (clock64() - t0 > p.wait_cycles) {
       tg_set_error(p, s, kDevTimeout, true);
       return false;
     }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import moe_megakernel_b200 as mk
-from tests.test_gpu_operators import BF, HF, U, act64, gradient, offsets_of, ortho_close, rand, slope64
+from tests.test_gpu_operators import BF, HF, U, act64, close, gradient, offsets_of, ortho_close, rand, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,29 @@ def test_results_on_an_explicit_stream_take_no_other_streams_memory(name):
     c = torch.full(shape, 7.0, dtype=BF, device="cuda")
     torch.cuda.synchronize()
     assert (c == 7).all()
+
+
+def _long_reduction(rows):
+    """x, dy [rows, 8], zeros but for some rows at the ends, in the middle and around them."""
+    g = torch.Generator().manual_seed(151)
+    at = torch.cat([torch.tensor([0, 1, 63, 64, rows // 2, rows - 65, rows - 2, rows - 1]),
+                    torch.randint(0, rows, (200,), generator=g)]).unique().cuda()
+    x, dy = (torch.zeros(rows, 8, dtype=BF, device="cuda") for _ in range(2))
+    x[at], dy[at] = rand(len(at), 8, seed=152), rand(len(at), 8, seed=153)
+    a, b = x[at].double(), dy[at].double()
+    return x, dy, a.T @ b, a.abs().T @ b.abs(), len(at)
+
+
+def test_reductions_of_most_of_a_billion_rows():
+    """One tile's reduction takes seconds, longer than any wait inside an ordinary call. Zero rows add
+    nothing, so the sum has the roundings of the other rows alone."""
+    rows = (3 << 28) + 37         # some 3.3 s in one tile, 6e9 cycles
+    x, dy, ref, S, n = _long_reduction(rows)
+    err = torch.zeros(2, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    dW = mk.grouped_matmul_wgrad(x, dy, off, error_word=err[:1])
+    torch.cuda.synchronize()
+    dense = mk.linear_backward(dy, x, dW[0], input_grad=False, error_word=err[1:])["dW"]
+    assert err.tolist() == [0, 0]
+    close(dW[0], ref, S, n)
+    close(dense, ref, S, n)
