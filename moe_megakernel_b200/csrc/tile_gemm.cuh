@@ -271,6 +271,9 @@ __device__ __forceinline__ TgTask tg_decode(int t, const TgParams& p, TgSmem& s)
 // Reduction steps (of 16) of k block kb.
 __device__ __forceinline__ int tg_ksteps(const TgTask& k, int kb) { return min(4, (k.klen - kb * 64 + 15) >> 4); }
 
+// The stream's earlier work is done and visible (programmatic stream serialisation).
+__device__ __forceinline__ void tg_after_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- list of tiles (warp 3)
 // A warp's place in the list.
 struct TgCursor {
@@ -330,6 +333,7 @@ __device__ void tg_schedule(const TgParams& p, TgSmem& s, TgState& at, int first
     __syncwarp();
     at.list.step();
     if (k.g < 0) return;
+    if (round == 0) tg_after_stream();   // before a wait that runs against the clock
     // round robin; tiles sorted by their time (ragged K) in turn from either end
     t = Mode == kTgRaggedK && (round & 1) == 0 ? (round + 1) * step + step - 1 - first : (round + 1) * step + first;
   }
@@ -1124,9 +1128,6 @@ __device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, Tg
 }
 
 // ---------------------------------------------------------------- kernel
-// The stream's earlier work is done and visible (programmatic stream serialisation).
-__device__ __forceinline__ void tg_after_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Barriers and TMEM; the caller synchronises the cluster afterwards.
 template <bool RaggedK>
 __device__ __forceinline__ void tg_setup(TgSmem& s, int stages, uint32_t rank) {
@@ -1160,8 +1161,9 @@ template <int Mode, bool PMn, bool QMn, int Epi, typename T>
 __device__ __forceinline__ void tg_product(const TgParams& p, const TgFactors& f, TgSmem& s, TgState& at, uint8_t* tiles,
                                            uint32_t tmem, uint32_t rank, int warp, int first, int end, int step) {
   const uint32_t base = ptx::smem_u32(tiles);
-  // the roles that touch global memory; the others set out under the end of the previous kernel
-  if (warp == 0 || warp >= 4) tg_after_stream();
+  // Warp 3 works its first tile out under the end of the previous kernel. The others touch global memory or
+  // wait for those that do, and a bounded wait must not run while that kernel does: it may take any time.
+  if (warp != 3) tg_after_stream();
   if (warp == 0) {
     tg_producer<Mode, PMn, QMn>(p, s, at, base, rank);
   } else if (warp == 1) {

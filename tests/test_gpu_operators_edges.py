@@ -178,3 +178,20 @@ def test_reductions_of_most_of_a_billion_rows():
     assert err.tolist() == [0, 0]
     close(dW[0], ref, S, n)
     close(dense, ref, S, n)
+
+
+def test_calls_queued_behind_seconds_of_work():
+    """The kernels of the calls that follow set out early, on the SMs that a one-tile reduction leaves idle,
+    and stand there for seconds: their waits count from its end. (No error words: zeroing one comes between.)"""
+    rows = (3 << 28) + 37
+    x, dy, ref, S, n = _long_reduction(rows)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    few = off.clamp(max=300)
+    torch.cuda.synchronize()
+    dW = mk.grouped_matmul_wgrad(x, dy, off)
+    up = mk.orthogonalize(dW[0])
+    other = mk.grouped_matmul(x[:300], dW, few)
+    close(dW[0], ref, S, n)
+    ortho_close(up, dW[0])
+    a, w = x[:300].double(), dW[0].double()
+    close(other, a @ w, a.abs() @ w.abs(), 8)
