@@ -172,10 +172,13 @@ __device__ __forceinline__ bool tg_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Cluster: the arrival is the peer CTA's and orders what it wrote to its shared memory.
+template <bool Cluster = false>
 __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, const TgParams& p, TgSmem& s) {
-  if (tg_try_wait(bar, parity)) return true;
+  auto arrived = [&] { return Cluster ? ptx::mbar_try_wait_cluster(bar, parity) : tg_try_wait(bar, parity); };
+  if (arrived()) return true;
   const long long t0 = clock64();
-  while (!tg_try_wait(bar, parity)) {
+  while (!arrived()) {
     if (*reinterpret_cast<volatile int*>(&s.abort)) return false;
     if (clock64() - t0 > p.wait_cycles) {
       tg_set_error(p, s, kDevTimeout, true);
@@ -184,8 +187,9 @@ __device__ __forceinline__ bool tg_wait(uint64_t* bar, uint32_t parity, const Tg
   }
   return true;
 }
+template <bool Cluster = false>
 __device__ __forceinline__ bool tg_wait_warp(uint64_t* bar, uint32_t parity, const TgParams& p, TgSmem& s) {
-  const bool ok = tg_wait(bar, parity, p, s);
+  const bool ok = tg_wait<Cluster>(bar, parity, p, s);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -456,7 +460,7 @@ __device__ void tg_tail_warp(const TgParams& p, TgSmem& s, TgState& at, uint8_t*
       if (rank != 0) {
         if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_u32(&s.peer_tail[last]), 0));
       } else {   // in place of the producer's arrival, once both CTAs' blocks are clean
-        if (!tg_wait_warp(&s.peer_tail[last], (used >> last) & 1, p, s)) return;
+        if (!tg_wait_warp<true>(&s.peer_tail[last], (used >> last) & 1, p, s)) return;
         if (lane == 0) ptx::mbar_arrive(&s.full[last]);
       }
       __syncwarp();

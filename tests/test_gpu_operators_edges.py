@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import moe_megakernel_b200 as mk
-from tests.test_gpu_operators import BF, HF, U, act64, close, gradient, offsets_of, ortho_close, rand, slope64
+from tests.test_gpu_operators import (BF, HF, U, act64, close, gradient, offsets_of, ortho_close, rand, slope64,
+                                      spans)
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +196,21 @@ def test_calls_queued_behind_seconds_of_work():
     ortho_close(up, dW[0])
     a, w = x[:300].double(), dW[0].double()
     close(other, a @ w, a.abs() @ w.abs(), 8)
+
+
+def test_ragged_tails_of_many_groups_give_the_same_bits():
+    """Every group ends inside a step of 16 rows, with infinities behind it: zeros that the follower of a
+    pair writes over the neighbour's rows are there before the leader multiplies them, in every run."""
+    g = torch.Generator().manual_seed(161)
+    counts = [int(c) for c in torch.randint(1, 400, (96,), generator=g)]
+    counts = [c + 1 if c % 16 == 0 else c for c in counts]
+    off, rows = offsets_of(counts), sum(counts)
+    x, dy = rand(rows, 264, seed=162), rand(rows, 328, seed=163)
+    last = torch.tensor([hi - 1 for _, _, hi in spans(off)[1::2]], device="cuda")   # of every other group
+    x[last], dy[last] = float("inf"), float("nan")
+    first = mk.grouped_matmul_wgrad(x, dy, off)
+    for e, lo, hi in spans(off)[0::2]:
+        a, b = x[lo:hi].double(), dy[lo:hi].double()
+        close(first[e], a.T @ b, a.abs().T @ b.abs(), hi - lo, f"group {e}")
+    for _ in range(30):
+        assert torch.equal(mk.grouped_matmul_wgrad(x, dy, off)[0::2], first[0::2])
