@@ -556,8 +556,9 @@ size_t moe_linear_backward_workspace_bytes(int T, int N, int activation, int bia
  *   X = G / (|G|_F + eps);  `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X
  * (X^T X on the right when m > n), with the step's a, b, c from the HOST array
  * coeffs [steps, 3]; out bf16 [m, n] (pitches ldo, bso) receives the last X.
- * X is carried to 19 bits (an fp16 value and 8 bits more); A, bA + cAA and X
- * enter the tensor-core products as fp16, accumulated in fp32. A and bA + cAA
+ * X is carried to 19 bits (an fp16 value and 8 bits more; entries below 2^-27
+ * to fewer, in steps of 2^-37 or less); A, bA + cAA and X enter the tensor-core
+ * products as fp16, accumulated in fp32. A and bA + cAA
  * (less a multiple of the identity) are stored times 1024, so their entries must
  * stay below 32 in magnitude (with the usual quintic coefficients below 7). A gradient of zeros gives zeros; an
  * infinity or NaN in a matrix makes that matrix's output NaN and no other's.

@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(256) moe_ortho_norm_kernel(const OrthoParams p
   if (threadIdx.x == 0) p.partial[blockIdx.y * kOrthoChunks + blockIdx.x] = s;
 }
 
-// X0 = G / (|G| + eps) as two factors: G times a power of two (exact in fp16 for
-// a bf16 gradient down to 2^-17 of the scale, with 8 bits more for an fp32 one),
-// and alpha = 2^E / (|G| + eps), which the first step's epilogues apply in fp32.
+// X0 = G / (|G| + eps) as two factors: G times a power of two, which brings the norm to 2^13 .. 2^14 (a bf16
+// entry is exact in fp16 down to 2^-30 of the norm, an fp32 one has 8 bits more down to 2^-27), and alpha =
+// 2^E / (|G| + eps), which the first step's epilogues apply in fp32.
 __device__ __forceinline__ double ortho_scale(const OrthoParams& p, double* scratch) {
   const double total =
       block_sum(threadIdx.x < p.chunks ? p.partial[blockIdx.y * kOrthoChunks + threadIdx.x] : 0.0, scratch);

@@ -762,7 +762,8 @@ __host__ __device__ constexpr int tg_epi_bytes(bool residual) { return kTgEpiWar
 // large ones at 3 bytes an entry. The 8 bits never leave this epilogue and lie
 // in the order its threads hold them: a piece is 32 lanes x 32 bytes.
 __device__ __forceinline__ int tg_low(float x, float h) { return (__float_as_int(x) - __float_as_int(h)) >> 5; }
-// Four of them as bytes (saturated: a tie rounded down leaves +128, and below fp16's normal numbers more).
+// Four of them as bytes (saturated: a tie rounded down leaves +128, and below fp16's normal numbers, 2^-27 of X,
+// more).
 __device__ __forceinline__ uint32_t tg_low4(int a, int b, int c, int d) {
   uint32_t hi, all;
   asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(d), "r"(c));

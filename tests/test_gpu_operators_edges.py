@@ -5,8 +5,8 @@ import pytest
 import torch
 
 import moe_megakernel_b200 as mk
-from tests.test_gpu_operators import (BF, HF, U, act64, close, gradient, offsets_of, ortho_close, rand, slope64,
-                                      spans)
+from tests.test_gpu_operators import (BF, HF, U, act64, close, gradient, offsets_of, ortho64, ortho_close, rand,
+                                      slope64, spans)
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +214,32 @@ def test_ragged_tails_of_many_groups_give_the_same_bits():
         close(first[e], a.T @ b, a.abs().T @ b.abs(), hi - lo, f"group {e}")
     for _ in range(30):
         assert torch.equal(mk.grouped_matmul_wgrad(x, dy, off)[0::2], first[0::2])
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("shape", [(192, 320), (320, 192), (40, 61), (2, 300, 520)])
+@pytest.mark.parametrize("spread", [1e6, 1e7])
+def test_orthogonalize_brings_small_rows_up(spread, shape, dtype):
+    """All rows but one (columns of a tall matrix) a millionth of the others' size and less, and a dozen
+    steps, which bring them to size: relative Frobenius error as of ortho_close for 12 steps, sqrt(36) * 8e-4
+    and 1.6e-3 in quadrature, 5.2e-3."""
+    g = torch.Generator(device="cuda").manual_seed(171)
+    G = torch.randn(shape, generator=g, device="cuda") * 1e-3
+    if shape[-2] > shape[-1]:
+        G[..., 3] *= spread
+    else:
+        G[..., 3, :] *= spread
+    G = G.to(dtype)
+    out, ref = mk.orthogonalize(G, steps=12), ortho64(G, steps=12)
+    size = ref.flatten(-2).norm(dim=-1)
+    err = (out.double() - ref).flatten(-2).norm(dim=-1)
+    assert (err <= 5.2e-3 * size).all(), (err / size).max()
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_orthogonalize_gradients_far_below_eps(dtype):
+    """A norm of 1e-12 beside an eps of 1e-7: X starts at 1e-5 and the steps bring it up. Tolerance as above."""
+    G = gradient(48, 80, seed=172)
+    G = (G * (1e-12 / G.norm())).to(dtype)
+    out, ref = mk.orthogonalize(G, steps=12), ortho64(G, steps=12)
+    assert (out.double() - ref).norm() <= 5.2e-3 * ref.norm()
