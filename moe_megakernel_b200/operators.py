@@ -132,6 +132,12 @@ def _workspace(nbytes: int, like, stream):
     return _new(like, (nbytes,), stream, torch.uint8) if nbytes else None
 
 
+def _apart(out, name: str, *inputs):
+    """A given result that starts where an input does would be written while the kernel still reads it."""
+    if out.numel() and any(t is not None and t.data_ptr() == out.data_ptr() for t in inputs):
+        raise ValueError(f"{name} overlaps an input")
+
+
 def _offsets(offsets, device):
     _tensor(offsets, "offsets", 1)
     groups = offsets.shape[0] - 1
@@ -148,8 +154,8 @@ def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, tran
 
     x [rows, K], W [groups, K, N] contiguous ([groups, N, K] with ``transpose``), offsets int32
     [groups + 1] on the device, not decreasing (``MoEPlan.routing``'s expert_offset fits; sizes
-    need no padding). Rows outside the groups are left as they were in a given y, undefined in a
-    new one. At most 1024 groups; K and N multiples of 8."""
+    need no padding). Rows outside the groups are left as they were in a given y (which overlaps
+    no input), undefined in a new one. At most 1024 groups; K and N multiples of 8."""
     _tensor(x, "x", 2)
     _tensor(W, "W", 3)
     dt = _half(x, "x")
@@ -165,6 +171,7 @@ def grouped_matmul(x: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, tran
         y = _new(x, (rows, N), stream)
     else:
         _like(y, "y", (rows, N), x.dtype, dev)
+        _apart(y, "y", x, W)
     _call("moe_grouped_matmul", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), offsets.data_ptr(), rows, groups, K, N,
           1 if transpose else 0, dt, y.data_ptr(), _pitch(y, "y"), _error_word(error_word, dev),
           _raw_stream(stream, dev))
@@ -191,6 +198,7 @@ def grouped_matmul_wgrad(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tenso
         dW = _new(x, (groups, K, N), stream)
     else:
         _whole(dW, "dW", (groups, K, N), x.dtype, dev)
+        _apart(dW, "dW", x, dy)
     _call("moe_grouped_matmul_wgrad", dev, x.data_ptr(), _pitch(x, "x"), dy.data_ptr(), _pitch(dy, "dy"),
           offsets.data_ptr(), rows, groups, K, N, dt, dW.data_ptr(), _error_word(error_word, dev),
           _raw_stream(stream, dev))
@@ -204,7 +212,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
 
     activation: None, "relu", "gelu" (erf), "gelu_tanh" or "silu". With ``save_preact`` (or a
     given ``preact``) returns (y, z), z = x @ W + bias as linear_backward takes it. y may be the
-    residual itself."""
+    residual itself; given results overlap nothing else."""
     _tensor(x, "x", 2)
     _tensor(W, "W", 2)
     dt, act = _half(x, "x"), _activation(activation)
@@ -223,8 +231,10 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
         y = _new(x, (T, N), stream)
     else:
         _like(y, "y", (T, N), x.dtype, dev)
+        _apart(y, "y", x, W, bias, preact)
     if preact is not None:
         _like(preact, "preact", (T, N), x.dtype, dev)
+        _apart(preact, "preact", x, W, bias, residual)
     elif save_preact:
         preact = _new(x, (T, N), stream)
     _call("moe_linear", dev, x.data_ptr(), _pitch(x, "x"), W.data_ptr(), _address(bias), _address(residual),
@@ -286,7 +296,9 @@ def orthogonalize(G: torch.Tensor, steps: int = 5,
     (weight gradients: ``MoEPlan.backward``'s dW1, dW3, dW2, ``grouped_matmul_wgrad``'s or
     ``linear_backward``'s dW). X = G / (|G|_F + eps), then ``steps`` times
     X <- a X + (b A + c A A) X with A = X X^T (the short side inside). G bf16 or fp32 of any size
-    and row pitch; returns bf16 of G's shape. coeffs: one (a, b, c) for all steps, or one per step."""
+    and row pitch; returns bf16 of G's shape (out may be a bf16 G itself). coeffs: one (a, b, c) for all
+    steps, or one per step. The entries of A and b A + c A A have to stay below 32 in magnitude (with
+    QUINTIC they stay below 7): they pass through fp16, and larger ones give infinities or NaN."""
     if not isinstance(G, torch.Tensor):
         raise TypeError("G must be a torch.Tensor")
     if G.dim() not in (2, 3) or G.shape[-1] < 1 or G.shape[-2] < 1:

@@ -243,3 +243,58 @@ def test_orthogonalize_gradients_far_below_eps(dtype):
     G = (G * (1e-12 / G.norm())).to(dtype)
     out, ref = mk.orthogonalize(G, steps=12), ortho64(G, steps=12)
     assert (out.double() - ref).norm() <= 5.2e-3 * ref.norm()
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("coeffs", [mk.QUINTIC, (1.0, 0.5, 0.25), (1.5, 0.5, 0.0), (2.0, 0.0, 0.0)])
+def test_orthogonalize_makes_a_matrix_with_an_infinity_nan_whatever_the_coefficients(coeffs, dtype):
+    G = gradient(4, 40, 72, seed=173).abs().to(dtype)
+    G[1, 7, 9] = float("inf")
+    G[2, 39, 71] = float("nan")
+    out = mk.orthogonalize(G, steps=2, coeffs=coeffs)
+    assert out[1].isnan().all() and out[2].isnan().all()
+    assert out[0].isfinite().all() and out[3].isfinite().all()
+    one = torch.full((1, 1), float("inf"), dtype=dtype, device="cuda")
+    assert mk.orthogonalize(one, steps=1, coeffs=coeffs).isnan().all()
+
+
+def test_captured_calls_with_error_words_and_a_forked_stream():
+    """A capture that holds zeroed error words between the kernels, and one whose calls run on a second
+    stream beside the first, replay to the plain calls' bits."""
+    x, W, off = rand(300, 512, seed=181), rand(4, 512, 264, seed=182, std=0.05), offsets_of([100, 0, 150, 50])
+    dy, z, G, W1 = rand(300, 264, seed=183), rand(300, 264, seed=184), gradient(3, 140, 100, seed=185), W[1].contiguous()
+    err = torch.full((6,), 9, dtype=torch.int32, device="cuda")
+
+    def work():
+        b = mk.linear_backward(dy, x, W1, preact=z, activation="gelu", bias_grad=True, error_word=err[0:1])
+        return [mk.grouped_matmul(x, W, off, error_word=err[1:2]),
+                mk.grouped_matmul_wgrad(x, dy, off, error_word=err[2:3]),
+                mk.linear(x, W1, activation="silu", error_word=err[3:4]), mk.linear(x[:3], W1, error_word=err[4:5]),
+                b["dx"], b["dW"], b["dbias"], mk.orthogonalize(G, error_word=err[5:6])]
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = work()
+    assert err.tolist() == [9] * 6
+    for _ in range(3):
+        graph.replay()
+    assert err.tolist() == [0] * 6
+    ref = work()
+    assert all(torch.equal(a, b) for a, b in zip(ref, outs))
+    side, forked = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(forked):
+        side.wait_stream(torch.cuda.current_stream())
+        y, u = mk.linear(x[:3], W1, stream=side), mk.orthogonalize(G, stream=side)
+        v = mk.grouped_matmul(x, W, off)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        forked.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(v, ref[0]) and torch.equal(y, ref[3]) and torch.equal(u, ref[7])
+
+
+def test_orthogonalize_in_place():
+    for shape in ((130, 90), (3, 90, 130)):
+        G = gradient(*shape, seed=191, dtype=BF)
+        ref = mk.orthogonalize(G)
+        assert mk.orthogonalize(G, out=G) is G and torch.equal(G, ref)

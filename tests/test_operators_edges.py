@@ -122,3 +122,27 @@ def test_extents_past_32_bits_are_refused(call, calls):
     with pytest.raises(mk.MoEError, match="MOE_ERR_UNSUPPORTED_SHAPE"):
         call(MetaStream())
     assert not calls
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, W, s: mk.grouped_matmul(x, W[None], _off(0, 8), y=x, stream=s),
+    lambda x, W, s: mk.grouped_matmul(x, W[None], _off(0, 8), y=W, stream=s),
+    lambda x, W, s: mk.grouped_matmul_wgrad(x, W, _off(0, 8), dW=x[None], stream=s),
+    lambda x, W, s: mk.grouped_matmul_wgrad(x, W, _off(0, 8), dW=W[None], stream=s),
+    lambda x, W, s: mk.linear(x, W, y=x, stream=s),
+    lambda x, W, s: mk.linear(x, W, y=W, stream=s),
+    lambda x, W, s: mk.linear(x, W, preact=x, stream=s),
+    lambda x, W, s: mk.linear(x, W, residual=_z(8, 8), preact=W, stream=s),
+    lambda x, W, s: (lambda r: mk.linear(x, W, residual=r, preact=r, stream=s))(_z(8, 8)),
+    lambda x, W, s: (lambda r: mk.linear(x, W, y=r, preact=r, stream=s))(_z(8, 8))])
+def test_results_on_top_of_inputs_are_refused(call, calls):
+    with pytest.raises(ValueError, match="overlaps"):
+        call(_z(8, 8), _z(8, 8), Stream())
+    assert not calls
+
+
+def test_results_that_may_share_memory(calls):
+    x, W, r = _z(8, 8), _z(8, 8), _z(8, 8)
+    assert mk.linear(x, W, residual=r, y=r, stream=Stream()) is r
+    assert mk.orthogonalize(x, out=x, stream=Stream()) is x
+    assert len(calls) == 2
