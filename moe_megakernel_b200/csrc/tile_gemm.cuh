@@ -301,7 +301,7 @@ struct TgCursor {
 };
 
 // Where a role stands in the rings of stages, accumulators and tiles; one per
-// warp, carried from product to product where a kernel runs several.
+// warp.
 struct TgState {
   int stage = 0;
   uint32_t phase = 0;
@@ -1030,8 +1030,9 @@ __device__ void tg_epilogue_plain(const TgParams& p, TgSmem& s, TgState& at, uin
 // a piece is stored, and the accumulator buffer is given back before the last
 // piece is.
 template <int Mode, int Epi, typename T>
-__device__ void tg_epilogue(const TgParams& p, const TgFactors& f, TgSmem& s, TgState& at, uint32_t store, uint32_t tmem,
-                            uint32_t rank, int warp) {
+__device__ void tg_epilogue(const TgParams& p, TgSmem& s, TgState& at, uint32_t store, uint32_t tmem, uint32_t rank,
+                            int warp) {
+  const TgFactors& f = p.factors;
   constexpr bool kWide = Epi == kTgUpdate || Epi == kTgUpdateOut;
   constexpr int kParts = kTgEpiWarps / 4;   // warps that share a quarter of the lanes, every kParts-th piece each
   const int lane = ptx::lane_id();
@@ -1163,8 +1164,9 @@ __device__ __forceinline__ void tg_setup(TgSmem& s, int stages, uint32_t rank) {
 
 // One product, all roles: tiles first, first + step, ... below end.
 template <int Mode, bool PMn, bool QMn, int Epi, typename T>
-__device__ __forceinline__ void tg_product(const TgParams& p, const TgFactors& f, TgSmem& s, TgState& at, uint8_t* tiles,
-                                           uint32_t tmem, uint32_t rank, int warp, int first, int end, int step) {
+__device__ __forceinline__ void tg_product(const TgParams& p, TgSmem& s, uint8_t* tiles, uint32_t tmem, uint32_t rank,
+                                           int warp, int first, int end, int step) {
+  TgState at;
   const uint32_t base = ptx::smem_u32(tiles);
   // Warp 3 works its first tile out under the end of the previous kernel. The others touch global memory or
   // wait for those that do, and a bounded wait must not run while that kernel does: it may take any time.
@@ -1179,7 +1181,7 @@ __device__ __forceinline__ void tg_product(const TgParams& p, const TgFactors& f
     tg_schedule<Mode>(p, s, at, first, end, step);
   } else {
     if (Epi == kTgPlain) tg_epilogue_plain<Mode, T>(p, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
-    else tg_epilogue<Mode, Epi, T>(p, f, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
+    else tg_epilogue<Mode, Epi, T>(p, s, at, base + p.stages * p.stage_bytes, tmem, rank, warp);
   }
   __syncwarp();
 }
@@ -1261,9 +1263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTgThreads, 1)
   ptx::cluster_sync();   // both CTAs' barriers exist before any remote arrive
   ptx::tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  TgState at;
-  tg_product<Mode, PMn, QMn, Epi, T>(p, p.factors, s, at, tiles, tmem, rank, warp, blockIdx.x >> 1, s.total,
-                                     gridDim.x >> 1);
+  tg_product<Mode, PMn, QMn, Epi, T>(p, s, tiles, tmem, rank, warp, blockIdx.x >> 1, s.total, gridDim.x >> 1);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();   // no peer still arrives on this CTA's barriers or reads its tiles

@@ -11,7 +11,9 @@ stream; its inputs have to be ready there, and a result that another stream goes
 on with needs what any tensor needs there: that stream waits, and
 ``Tensor.record_stream`` if the result may be dropped before that work is done.
 `error_word`, an int32 tensor of one element, receives the call's device error
-code (0 = none).
+code (0 = none). Results carry no autograd history, whether the inputs require
+gradients or not: ``linear_backward``, ``grouped_matmul_wgrad`` and the transposed
+``grouped_matmul`` are the backward passes.
 """
 from __future__ import annotations
 
