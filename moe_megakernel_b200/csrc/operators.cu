@@ -683,10 +683,13 @@ extern "C" int moe_orthogonalize(const void* G, long long ldg, long long bsg, in
   if (tri >= (1ll << 30) || tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   // B is stored less a multiple d of the identity, X' = (a + d) X + (B - d I) X: once the singular values are
   // near 1, B's eigenvalues lie within a few tenths of b + c = -2.7, and the fp16 roundings of B and X enter X'
-  // times what is left of B. d is B's eigenvalue at the root mean square of the singular values, which starts
-  // at 1 / sqrt(p) and is followed through the steps (a guess: any d is exact up to rounding). Error against
-  // 64 bits of a 28 x 1835 matrix without it 2.5e-3, of which bf16's own rounding is 1.7e-3.
-  double sigma = 1.0 / std::sqrt((double)p0);
+  // times what is left of B. d is B's eigenvalue at a singular value that is followed through the steps (a
+  // guess: any d is exact up to rounding). Too large a guess costs the directions that are still small: their B
+  // is near 0, and a rounding of X as a whole enters them times d. So it starts at a tenth of the root mean
+  // square 1 / sqrt(p), or at 1 / p where that is more (p = 1: 1 itself). Errors against 64 bits of a 28 x 1835
+  // matrix: without d 2.2e-3 (bf16's own rounding is 1.65e-3), from the root mean square 1.9e-3, from here
+  // 1.8e-3; of one direction a thousand times the others, 20 x 30: 1.7e-3, 6.3e-3, 2.3e-3.
+  double sigma = std::max(0.1, 1.0 / std::sqrt((double)p0)) / std::sqrt((double)p0);
   for (int i = 0; i < steps; ++i) {
     const double ca = coeffs[3 * i], cb = coeffs[3 * i + 1], cc = coeffs[3 * i + 2];
     const double t = std::min(1.0, sigma * sigma);

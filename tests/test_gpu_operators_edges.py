@@ -298,3 +298,16 @@ def test_orthogonalize_in_place():
         G = gradient(*shape, seed=191, dtype=BF)
         ref = mk.orthogonalize(G)
         assert mk.orthogonalize(G, out=G) is G and torch.equal(G, ref)
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("m,n,spread", [(20, 30, 1e3), (30, 20, 1e3), (40, 60, 1e4), (200, 300, 1e4)])
+def test_orthogonalize_of_one_direction_far_above_the_others(m, n, spread, dtype):
+    """The other directions, among few of which a rounding of the large one's entries spreads, keep the
+    accuracy of ortho_close. (A bf16 gradient has rounded them itself; the 64-bit form starts from that.)"""
+    g = torch.Generator(device="cuda").manual_seed(201)
+    u, v = (torch.linalg.qr(torch.randn(k, k, device="cuda", dtype=torch.float64, generator=g))[0] for k in (m, n))
+    s = torch.full((min(m, n),), 1 / spread, device="cuda", dtype=torch.float64)
+    s[0] = 1.0
+    G = ((u[:, :len(s)] * s) @ v[:len(s)]).to(dtype)
+    ortho_close(mk.orthogonalize(G), G)
