@@ -41,14 +41,14 @@ __device__ __forceinline__ float act_slope(float z) {
     // q(v) + z q (1 - q) v'(z). z q (1 - q) is formed first and v' bounded (from |z| = 473 on, long after
     // q is 0 or 1): a zero then never meets an infinity, however large z is
     const float w = fminf(0.044715f * z * z, 1e4f);
-    float rest;
-    const float q = tg_sigmoid(1.59576912160573071f * fmaf(w, z, z), rest);
-    return fmaf(q * rest * z, 1.59576912160573071f * fmaf(3.f, w, 1.f), q);
+    float slope;
+    const float q = tg_sigmoid(1.59576912160573071f * fmaf(w, z, z), slope);
+    return fmaf(slope * z, 1.59576912160573071f * fmaf(3.f, w, 1.f), q);
   }
   if (Act == kActSilu) {
-    float rest;
-    const float q = tg_sigmoid(z, rest);
-    return q * fmaf(z, rest, 1.f);
+    float slope;
+    const float q = tg_sigmoid(z, slope);
+    return fmaf(z, slope, q);
   }
   return 1.f;
 }
