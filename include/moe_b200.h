@@ -492,8 +492,10 @@ int moe_plan_forward_launches(moe_plan_t plan, int fp8);
  * accumulated in fp32 on the tensor cores; a result is rounded once, to nearest.
  *
  * error_word: device int32 [1], or NULL. It is zeroed by the call and receives
- * the call's device error code (0 = none, 1 = a bounded wait ran out,
- * 2 = group offsets out of order or out of range).
+ * the call's device error code (0 = none, 1 = a bounded wait ran out: two
+ * seconds, and more with the length of the reduction, 2 = group offsets out of
+ * order or out of range). Without one such a call ends unmarked.
+ * Outputs overlap no input and each other, except where a call says so.
  *
  * Common errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, bad pitch,
  * unknown type or activation, negative count), MOE_ERR_UNSUPPORTED_SHAPE (K or N
@@ -555,7 +557,8 @@ size_t moe_linear_backward_workspace_bytes(int T, int N, int activation, int bia
  * `dtype` bf16 or fp32, row pitch ldg >= n and batch pitch bsg in elements)
  *   X = G / (|G|_F + eps);  `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X
  * (X^T X on the right when m > n), with the step's a, b, c from the HOST array
- * coeffs [steps, 3]; out bf16 [m, n] (pitches ldo, bso) receives the last X.
+ * coeffs [steps, 3]; out bf16 [m, n] (pitches ldo, bso) receives the last X; it
+ * may be a bf16 G itself.
  * X is carried to 19 bits (an fp16 value and 8 bits more; entries below 2^-27
  * to fewer, in steps of 2^-37 or less); A, bA + cAA and X enter the tensor-core
  * products as fp16, accumulated in fp32. A and bA + cAA

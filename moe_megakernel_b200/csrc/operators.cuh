@@ -56,7 +56,7 @@ __device__ __forceinline__ float act_slope(float z) {
 // dz = dy act'(z), rounded once to the operand type of the two products that
 // read it (half the width of an fp32 dz, and the tensor cores take no other), and
 // this chunk's column sums of the unrounded dz. 4093 x 7168 with the erf slope:
-// 42 us for 176 MB (4.2 TB/s).
+// 38 us for 176 MB (4.6 TB/s), 29 with relu.
 template <int Act, typename T>
 __device__ __forceinline__ void act_rows(const ActParams& p, int col, int first, int last, float (&acc)[8]) {
   const T* dy = reinterpret_cast<const T*>(p.dy);

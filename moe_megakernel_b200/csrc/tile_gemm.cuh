@@ -28,7 +28,7 @@
 // shared by few pairs at a time a k block takes 600 to 750 cycles. 8192 x 4096 ->
 // 14336 features, bf16: 609 us (1.58 PFLOP/s) in a burst and 718 us (1.34) under
 // the 1 kW cap, where the clock settles near 1.2 GHz; the library's plain product
-// of the same matrices 628 and 716 us on the same GPU. Tensor pipe busy 85 to 89 %
+// of the same matrices 628 and 716 us on the same GPU. Tensor pipe busy 85 to 87 %
 // of the cycles (dense 4096 x 4096 -> 14336 and 128 uneven groups, ncu). Tiles of
 // 256 columns are the largest with two accumulators in TMEM; smaller ones load
 // more a FLOP (see pick_tile in operators.cu).
