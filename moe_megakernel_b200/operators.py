@@ -234,6 +234,8 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     else:
         _like(y, "y", (T, N), x.dtype, dev)
         _apart(y, "y", x, W, bias, preact)
+        if residual is not None and residual.data_ptr() == y.data_ptr() and residual.stride() != y.stride() and T > 1:
+            raise ValueError("y overlaps the residual, in rows of another pitch")
     if preact is not None:
         _like(preact, "preact", (T, N), x.dtype, dev)
         _apart(preact, "preact", x, W, bias, residual)

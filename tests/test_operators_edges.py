@@ -134,7 +134,8 @@ def test_extents_past_32_bits_are_refused(call, calls):
     lambda x, W, s: mk.linear(x, W, preact=x, stream=s),
     lambda x, W, s: mk.linear(x, W, residual=_z(8, 8), preact=W, stream=s),
     lambda x, W, s: (lambda r: mk.linear(x, W, residual=r, preact=r, stream=s))(_z(8, 8)),
-    lambda x, W, s: (lambda r: mk.linear(x, W, y=r, preact=r, stream=s))(_z(8, 8))])
+    lambda x, W, s: (lambda r: mk.linear(x, W, y=r, preact=r, stream=s))(_z(8, 8)),
+    lambda x, W, s: (lambda r: mk.linear(x, W, y=r[:8], residual=r.view(8, 16)[:, :8], stream=s))(_z(16, 8))])
 def test_results_on_top_of_inputs_are_refused(call, calls):
     with pytest.raises(ValueError, match="overlaps"):
         call(_z(8, 8), _z(8, 8), Stream())
